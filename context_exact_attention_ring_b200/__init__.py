@@ -13,6 +13,9 @@ Names follow the C ABI:
   ring_attn_decode_partial, ring_attn_merge, ring_attn_decode,
   ring_attn_decode_workspace_bytes, ring_attn_decode_fused,
   ring_attn_kv_append, ring_attn_sched_stats, ring_attn_device_error;
+  ring_attn_page_extend, ring_attn_page_trim, ring_attn_paged_append,
+  ring_attn_decode_paged, ring_attn_page_bounds, ring_attn_page_scores,
+  ring_attn_page_select (the paged KV cache);
 and ring_attention (RingAttnFunction), the forward and backward under autograd.
 """
 from __future__ import annotations
@@ -44,6 +47,8 @@ EXPORTED = (
     "ring_attn_version", "ring_attn_built_arch", "ring_attn_selftest_wait", "ring_attn_decode_partial_noalloc",
     "ring_attn_decode_fused", "ring_attn_kv_append", "ring_attn_bwd", "ring_attn_bwd_delta",
     "ring_attn_bwd_workspace_bytes", "ring_attn_step_bwd", "ring_attn_bwd_simt",
+    "ring_attn_page_extend", "ring_attn_page_trim", "ring_attn_paged_append", "ring_attn_decode_paged_workspace_bytes",
+    "ring_attn_decode_paged", "ring_attn_page_bounds", "ring_attn_page_scores", "ring_attn_page_select",
 )
 
 
@@ -96,6 +101,13 @@ def lib():
         "ring_attn_version": [],
         "ring_attn_selftest_wait": [i32, vp],
         "ring_attn_built_arch": [],
+        "ring_attn_page_extend": [vp] * 8 + [i32, i32, sz, i32, i32, i32, vp],
+        "ring_attn_page_trim": [vp] * 5 + [i32, i32, sz, i32, i32, vp],
+        "ring_attn_paged_append": [vp] * 5 + [i32] * 5 + [sz] * 5 + [i32, vp],
+        "ring_attn_decode_paged": [vp] * 9 + [i32] * 8 + [sz] * 6 + [f32, i32, i32, vp, sz, vp],
+        "ring_attn_page_bounds": [vp] * 5 + [i32] * 6 + [sz] * 4 + [i32, vp],
+        "ring_attn_page_scores": [vp] * 5 + [i32] * 7 + [sz] * 3 + [i32, vp],
+        "ring_attn_page_select": [vp] * 4 + [i32] * 7 + [vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -106,6 +118,8 @@ def lib():
     L.ring_attn_decode_workspace_bytes.restype = sz
     L.ring_attn_bwd_workspace_bytes.argtypes = [i32] * 3
     L.ring_attn_bwd_workspace_bytes.restype = sz
+    L.ring_attn_decode_paged_workspace_bytes.argtypes = [i32]
+    L.ring_attn_decode_paged_workspace_bytes.restype = sz
     _lib = L
     return L
 
@@ -458,6 +472,230 @@ def ring_attn_kv_append(k_cache, v_cache, k_new, v_new, shard_lens, n_appended, 
                                    _ptr(n_appended), B, T, Hkv, Smax, D, int(P), int(block),
                                    _dtype_code(k_cache), _stream())
     _check(st, "ring_attn_kv_append")
+
+
+# ---------------------------------------------------------------------------
+# paged KV cache (layouts and rules: include/ring_attn.h)
+# ---------------------------------------------------------------------------
+def _one_device(*ts):
+    """The CUDA device all given tensors live on."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must live on a CUDA device")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors must live on one device")
+    return dev
+
+
+def _launch(name, dev, *args):
+    """Call the library on the tensors' device, on that device's current torch stream."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    _check(st, name)
+
+
+def _int32(what, t, shape):
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
+    return t.data_ptr()
+
+
+def _table(block_table, B=None):
+    """(pointer, W, row stride) of a block table [B, W] (rows may be slices of wider ones)."""
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1 and block_table.shape[1] > 1 \
+            or (B is not None and block_table.shape[0] != B):
+        raise ValueError("block_table must be int32 [B, W] with contiguous rows")
+    n, W = block_table.shape
+    return block_table.data_ptr(), W, block_table.stride(0) if n > 1 else max(W, 1)
+
+
+def _pool(k_pool, v_pool=None):
+    """(num_pages, page_size, Hkv, D, page, token and head strides) of cache pools [num_pages, page_size, Hkv, D]."""
+    if k_pool.dim() != 4 or k_pool.stride(3) != 1:
+        raise ValueError("pools must be [num_pages, page_size, Hkv, D] with contiguous last dimension")
+    if v_pool is not None and (v_pool.shape != k_pool.shape or v_pool.stride() != k_pool.stride() or
+                               v_pool.dtype != k_pool.dtype):
+        raise ValueError("k_pool and v_pool must have one shape, dtype and strides")
+    N, ps, Hkv, D = k_pool.shape
+    sp, st, sh, _ = k_pool.stride()
+    # the stride of a dimension of length 1 says nothing
+    return N, ps, Hkv, D, (sp if N > 1 else ps * st), (st if ps > 1 else Hkv * D), (sh if Hkv > 1 else D)
+
+
+def _rows3(what, x, shape, dtype):
+    """(row stride, head stride) of x [n, heads, D] with contiguous D."""
+    if tuple(x.shape) != shape or x.dtype != dtype or x.stride(2) != 1:
+        raise ValueError(f"{what} must be {list(shape)} of the cache's dtype with contiguous last dimension")
+    return (x.stride(0) if shape[0] > 1 else shape[1] * shape[2]), (x.stride(1) if shape[1] > 1 else shape[2])
+
+
+def ring_attn_page_extend(seq_lens, new_lens, block_table, free_pages, n_free, page_size, max_tokens=None,
+                          slot_map=None, start_lens=None, cu_new=None):
+    """Pages and cache rows for new_lens[b] new tokens of every sequence, on the
+    device: seq_lens [B], block_table [B,W] and n_free [1] (pages on the free
+    list free_pages) advance in place.  Returns (slot_map, start_lens, cu_new);
+    slot_map has max_tokens entries (give one of the two), -1 past the call's
+    tokens and for sequences that found no room (start_lens -1,
+    ring_attn_device_error() RING_ECAPACITY)."""
+    dev = _one_device(seq_lens, new_lens, block_table, free_pages, n_free, slot_map, start_lens, cu_new)
+    B = seq_lens.numel()
+    tp, W, ts = _table(block_table, B)
+    if slot_map is None:
+        if max_tokens is None:
+            raise ValueError("give max_tokens or slot_map")
+        slot_map = torch.empty((int(max_tokens),), device=dev, dtype=torch.int32)
+    elif max_tokens is not None and slot_map.numel() != int(max_tokens):
+        raise ValueError("slot_map must have max_tokens entries")
+    if start_lens is None:
+        start_lens = torch.empty((B,), device=dev, dtype=torch.int32)
+    if cu_new is None:
+        cu_new = torch.empty((B + 1,), device=dev, dtype=torch.int32)
+    n, T = free_pages.numel(), slot_map.numel()
+    _launch("ring_attn_page_extend", dev, _int32("seq_lens", seq_lens, (B,)), _int32("new_lens", new_lens, (B,)), tp,
+            _int32("free_pages", free_pages, (n,)), _int32("n_free", n_free, (1,)),
+            _int32("slot_map", slot_map, (T,)), _int32("start_lens", start_lens, (B,)),
+            _int32("cu_new", cu_new, (B + 1,)), B, W, ts, int(page_size), n, T)
+    return slot_map, start_lens, cu_new
+
+
+def ring_attn_page_trim(seq_lens, keep_lens, block_table, free_pages, n_free, page_size):
+    """Cut every sequence to keep_lens[b] tokens (0 ends it) and give the pages
+    past its new end back to the free list, in place."""
+    dev = _one_device(seq_lens, keep_lens, block_table, free_pages, n_free)
+    B = seq_lens.numel()
+    tp, W, ts = _table(block_table, B)
+    n = free_pages.numel()
+    _launch("ring_attn_page_trim", dev, _int32("seq_lens", seq_lens, (B,)), _int32("keep_lens", keep_lens, (B,)), tp,
+            _int32("free_pages", free_pages, (n,)), _int32("n_free", n_free, (1,)), B, W, ts, int(page_size), n)
+
+
+def ring_attn_paged_append(k_pool, v_pool, k_new, v_new, slot_map):
+    """Write k_new / v_new [T,Hkv,D] into the rows slot_map [T] of the cache
+    pools (slots outside the pools, -1 for instance, are skipped)."""
+    dev = _one_device(k_pool, v_pool, k_new, v_new, slot_map)
+    N, ps, Hkv, D, sp, st, sh = _pool(k_pool, v_pool)
+    T = slot_map.numel()
+    nt, nh = _rows3("k_new", k_new, (T, Hkv, D), k_pool.dtype)
+    if _rows3("v_new", v_new, (T, Hkv, D), k_pool.dtype) != (nt, nh):
+        raise ValueError("k_new and v_new must have the same strides")
+    _launch("ring_attn_paged_append", dev, k_pool.data_ptr(), v_pool.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+            _int32("slot_map", slot_map, (T,)), T, Hkv, D, N, ps, sp, st, sh, nt, nh, _dtype_code(k_pool))
+
+
+def ring_attn_decode_paged_workspace_bytes(D) -> int:
+    return int(lib().ring_attn_decode_paged_workspace_bytes(int(D)))
+
+
+def decode_paged_workspace(D, device="cuda"):
+    """A zeroed workspace for ring_attn_decode_paged (one per stream; allocated with torch)."""
+    n = ring_attn_decode_paged_workspace_bytes(D)
+    if n == 0:
+        raise ValueError("bad head dimension")
+    return torch.zeros(n, device=device, dtype=torch.uint8)
+
+
+def ring_attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, sel=None, n_sel=None, scale=None, out=None,
+                           out_lse=None, workspace=None, out_dtype=None):
+    """Attention of q [B,Hq,D] (one new token per sequence) over the seq_lens[b]
+    keys of its cache pages, or over the pages sel [B,Hkv,K] / n_sel [B,Hkv]
+    list for each kv head.  Returns (out, out_lse)."""
+    dev = _one_device(q, k_pool, v_pool, block_table, seq_lens, sel, n_sel, out, out_lse, workspace)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, D]")
+    B, Hq, D = q.shape
+    N, ps, Hkv, Dk, sp, st, sh = _pool(k_pool, v_pool)
+    qb, qh = _rows3("q", q, (B, Hq, Dk), k_pool.dtype)
+    tp, W, ts = _table(block_table, B)
+    if (sel is None) != (n_sel is None):
+        raise ValueError("give both sel and n_sel, or neither")
+    K, selp, nselp = 0, None, None
+    if sel is not None:
+        K = sel.shape[-1] if sel.dim() else 0
+        selp, nselp = _int32("sel", sel, (B, Hkv, K)), _int32("n_sel", n_sel, (B, Hkv))
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    if out is None:
+        out = torch.empty((B, Hq, D), device=dev, dtype=out_dtype or q.dtype)
+    elif tuple(out.shape) != (B, Hq, D) or not out.is_contiguous() or (out_dtype or out.dtype) != out.dtype:
+        raise ValueError("out must be contiguous [B, Hq, D] of out_dtype")
+    if out_lse is None:
+        out_lse = torch.empty((B, Hq), device=dev, dtype=torch.float32)
+    elif tuple(out_lse.shape) != (B, Hq) or out_lse.dtype != torch.float32 or not out_lse.is_contiguous():
+        raise ValueError("out_lse must be contiguous float32 [B, Hq]")
+    if workspace is None:
+        workspace = decode_paged_workspace(D, dev)
+    elif not workspace.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    _launch("ring_attn_decode_paged", dev, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), tp,
+            _int32("seq_lens", seq_lens, (B,)), selp, nselp, out.data_ptr(), out_lse.data_ptr(), B, Hq, Hkv, D, N, ps,
+            W, K, qb, qh, sp, st, sh, ts, scale, _dtype_code(q), _dtype_code(out), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return out, out_lse
+
+
+def ring_attn_page_bounds(k_pool, block_table, seq_lens, bounds=None, start_lens=None):
+    """Minimum and maximum of the keys of every page, per kv head: bounds
+    [num_pages,Hkv,2,D], brought up to date for the pages that hold tokens from
+    start_lens[b] on (all pages without it).  Returns bounds."""
+    dev = _one_device(k_pool, block_table, seq_lens, bounds, start_lens)
+    N, ps, Hkv, D, sp, st, sh = _pool(k_pool)
+    B = seq_lens.numel()
+    tp, W, ts = _table(block_table, B)
+    if bounds is None:
+        bounds = torch.zeros((N, Hkv, 2, D), device=dev, dtype=k_pool.dtype)
+    elif tuple(bounds.shape) != (N, Hkv, 2, D) or bounds.dtype != k_pool.dtype or not bounds.is_contiguous():
+        raise ValueError("bounds must be contiguous [num_pages, Hkv, 2, D] of the cache's dtype")
+    _launch("ring_attn_page_bounds", dev, k_pool.data_ptr(), bounds.data_ptr(), tp,
+            _int32("seq_lens", seq_lens, (B,)),
+            None if start_lens is None else _int32("start_lens", start_lens, (B,)), B, Hkv, D, N, ps, W, sp, st, sh,
+            ts, _dtype_code(k_pool))
+    return bounds
+
+
+def ring_attn_page_scores(q, bounds, block_table, seq_lens, page_size, scores=None):
+    """scores [B,Hkv,W]: for every page an upper bound of q . k over its keys and
+    the query heads of the kv head (-inf past the sequence's pages)."""
+    dev = _one_device(q, bounds, block_table, seq_lens, scores)
+    if q.dim() != 3 or bounds.dim() != 4 or bounds.shape[2] != 2 or not bounds.is_contiguous():
+        raise ValueError("q [B, Hq, D] and contiguous bounds [num_pages, Hkv, 2, D] expected")
+    B, Hq, _ = q.shape
+    N, Hkv, _, D = bounds.shape
+    qb, qh = _rows3("q", q, (B, Hq, D), bounds.dtype)
+    tp, W, ts = _table(block_table, B)
+    if scores is None:
+        scores = torch.empty((B, Hkv, W), device=dev, dtype=torch.float32)
+    elif tuple(scores.shape) != (B, Hkv, W) or scores.dtype != torch.float32 or not scores.is_contiguous():
+        raise ValueError("scores must be contiguous float32 [B, Hkv, W]")
+    _launch("ring_attn_page_scores", dev, q.data_ptr(), bounds.data_ptr(), tp, _int32("seq_lens", seq_lens, (B,)),
+            scores.data_ptr(), B, Hq, Hkv, D, N, int(page_size), W, qb, qh, ts, _dtype_code(q))
+    return scores
+
+
+def ring_attn_page_select(scores, seq_lens, page_size, K, keep_first=1, keep_last=1, sel=None, n_sel=None):
+    """The K best-scored pages per (sequence, kv head) of scores [B,Hkv,W], the
+    first keep_first and last keep_last of the sequence always among them.
+    Returns (sel [B,Hkv,K] ascending, then -1; n_sel [B,Hkv])."""
+    dev = _one_device(scores, seq_lens, sel, n_sel)
+    if scores.dim() != 3 or scores.dtype != torch.float32 or not scores.is_contiguous():
+        raise ValueError("scores must be contiguous float32 [B, Hkv, W]")
+    B, Hkv, W = scores.shape
+    K = int(K)
+    if sel is None:
+        sel = torch.empty((B, Hkv, K), device=dev, dtype=torch.int32)
+    if n_sel is None:
+        n_sel = torch.empty((B, Hkv), device=dev, dtype=torch.int32)
+    _launch("ring_attn_page_select", dev, scores.data_ptr(), _int32("seq_lens", seq_lens, (B,)),
+            _int32("sel", sel, (B, Hkv, K)), _int32("n_sel", n_sel, (B, Hkv)), B, Hkv, W, int(page_size), K,
+            int(keep_first), int(keep_last))
+    return sel, n_sel
 
 
 class RingAttnFunction(torch.autograd.Function):

@@ -531,7 +531,7 @@ const char* ring_attn_strerror(ring_status s) {
     case RING_EUNSUPPORTED: return "unsupported configuration";
     case RING_ECUDA: return "CUDA error";
     case RING_ETIMEOUT: return "a bounded wait inside a kernel expired";
-    case RING_ECAPACITY: return "a KV append found its shard full";
+    case RING_ECAPACITY: return "a KV append found its shard full, or a page extend its free list empty";
   }
   return "unknown status";
 }

@@ -1,0 +1,235 @@
+// C ABI of the paged-cache operators (declared in include/ring_attn.h):
+// argument checks and dispatch.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/ring_attn.h"
+#include "kernels.h"
+#include "paged.h"
+
+using namespace ra;
+
+namespace {
+
+bool aligned(const void* p, unsigned a) { return p && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+ring_status from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return RING_OK;
+  if (e == cudaErrorNotSupported) return RING_EUNSUPPORTED;
+  if (e == cudaErrorInvalidValue) return RING_EINVAL;
+  return RING_ECUDA;
+}
+
+// log2 of a page size: a power of two in [RING_PAGE_MIN, RING_PAGE_MAX]; -1 otherwise.
+int page_log2(int ps) {
+  if (ps < RING_PAGE_MIN || ps > RING_PAGE_MAX || (ps & (ps - 1))) return -1;
+  int l = 0;
+  while ((1 << l) < ps) ++l;
+  return l;
+}
+
+bool good_dtype(int dtype) { return dtype == RING_BF16 || dtype == RING_FP32; }
+int elem_bytes(int dtype) { return dtype == RING_BF16 ? 2 : 4; }
+
+// A sequence's positions, and the slots of a pool, are 32-bit numbers.
+bool table_fits(int W, int ps_log2) { return ((long long)W << ps_log2) <= 0x7fffff00LL; }
+
+// Strides (elements) of rows of 16-byte pieces, far below 2^40 bytes.
+bool good_stride(size_t s, int eb) { return s < (size_t(1) << 36) && (s * eb) % 16 == 0; }
+
+// Strides of [n, heads, D] rows.
+bool good_rows(size_t sn, size_t sh, int n, int heads, int D, int eb) {
+  return good_stride(sn, eb) && good_stride(sh, eb) && (n == 1 || sn >= (size_t)D) && (heads == 1 || sh >= (size_t)D);
+}
+
+ring_status pool_check(const void* pool, int num_pages, int ps_log2, int Hkv, int D, size_t sp, size_t st, size_t sh,
+                       int dtype, PoolStrides* out) {
+  if (!aligned(pool, 16) || num_pages < 1 || Hkv < 1 || D < 1 || !good_dtype(dtype)) return RING_EINVAL;
+  if (!table_fits(num_pages, ps_log2)) return RING_EINVAL;
+  if (D != 64 && D != 128) return RING_EUNSUPPORTED;
+  const int eb = elem_bytes(dtype);
+  if (!good_stride(sp, eb) || !good_stride(st, eb) || !good_stride(sh, eb)) return RING_EINVAL;
+  // rows of different heads, tokens and pages may not overlap
+  if (st < (size_t)D || (Hkv > 1 && sh < (size_t)D) || (num_pages > 1 && sp < (size_t)D)) return RING_EINVAL;
+  out->page = (long long)sp;
+  out->token = (long long)st;
+  out->head = (long long)sh;
+  return RING_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ring_status ring_attn_page_extend(int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table,
+                                  const int32_t* free_pages, int32_t* n_free, int32_t* slot_map, int32_t* start_lens,
+                                  int32_t* cu_new, int B, int W, size_t table_stride, int page_size, int max_free,
+                                  int max_tokens, void* stream) {
+  if (!aligned(seq_lens, 4) || !aligned(new_lens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
+      !aligned(n_free, 4) || !aligned(slot_map, 4) || !aligned(start_lens, 4) || !aligned(cu_new, 4))
+    return RING_EINVAL;
+  if (B < 1 || W < 1 || max_free < 1 || max_tokens < 1 || page_size < 1 || table_stride < (size_t)W) return RING_EINVAL;
+  const int pl = page_log2(page_size);
+  if (pl < 0) return RING_EUNSUPPORTED;
+  if (!table_fits(W, pl) || table_stride >= (size_t(1) << 32)) return RING_EINVAL;
+  ExtendArgs a{};
+  a.seq_lens = seq_lens; a.new_lens = new_lens; a.table = block_table; a.free_pages = free_pages; a.n_free = n_free;
+  a.slot_map = slot_map; a.start_lens = start_lens; a.cu_new = cu_new;
+  a.table_stride = (long long)table_stride;
+  a.B = B; a.W = W; a.ps_log2 = pl; a.max_free = max_free; a.max_tokens = max_tokens;
+  a.err = error_word();
+  return from_cuda(launch_page_extend(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ring_status ring_attn_page_trim(int32_t* seq_lens, const int32_t* keep_lens, const int32_t* block_table,
+                                int32_t* free_pages, int32_t* n_free, int B, int W, size_t table_stride,
+                                int page_size, int max_free, void* stream) {
+  if (!aligned(seq_lens, 4) || !aligned(keep_lens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
+      !aligned(n_free, 4))
+    return RING_EINVAL;
+  if (B < 1 || W < 1 || max_free < 1 || page_size < 1 || table_stride < (size_t)W) return RING_EINVAL;
+  const int pl = page_log2(page_size);
+  if (pl < 0) return RING_EUNSUPPORTED;
+  if (!table_fits(W, pl) || table_stride >= (size_t(1) << 32)) return RING_EINVAL;
+  TrimArgs a{};
+  a.seq_lens = seq_lens; a.keep_lens = keep_lens; a.table = block_table; a.free_pages = free_pages; a.n_free = n_free;
+  a.table_stride = (long long)table_stride;
+  a.B = B; a.W = W; a.ps_log2 = pl; a.max_free = max_free;
+  a.err = error_word();
+  return from_cuda(launch_page_trim(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ring_status ring_attn_paged_append(void* k_pool, void* v_pool, const void* k_new, const void* v_new,
+                                   const int32_t* slot_map, int T, int Hkv, int D, int num_pages, int page_size,
+                                   size_t stride_page, size_t stride_token, size_t stride_head, size_t new_token,
+                                   size_t new_head, int dtype, void* stream) {
+  if (!aligned(v_pool, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(slot_map, 4)) return RING_EINVAL;
+  if (T < 1 || page_size < 1) return RING_EINVAL;
+  const int pl = page_log2(page_size);
+  if (pl < 0) return RING_EUNSUPPORTED;
+  PagedAppendArgs a{};
+  const ring_status rs = pool_check(k_pool, num_pages, pl, Hkv, D, stride_page, stride_token, stride_head, dtype,
+                                    &a.pool);
+  if (rs != RING_OK) return rs;
+  a.elem_bytes = elem_bytes(dtype);
+  if (!good_rows(new_token, new_head, T, Hkv, D, a.elem_bytes)) return RING_EINVAL;
+  if ((long long)Hkv * D > (1LL << 24)) return RING_EINVAL;
+  a.k_pool = k_pool; a.v_pool = v_pool; a.k_new = k_new; a.v_new = v_new; a.slot_map = slot_map;
+  a.new_token = (long long)new_token;
+  a.new_head = (long long)new_head;
+  a.T = T; a.Hkv = Hkv; a.D = D; a.num_pages = num_pages; a.ps_log2 = pl;
+  return from_cuda(launch_paged_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t ring_attn_decode_paged_workspace_bytes(int D) {
+  if (D != 64 && D != 128) return 0;
+  return paged_decode_workspace_bytes(D);
+}
+
+ring_status ring_attn_decode_paged(const void* q, const void* k_pool, const void* v_pool, const int32_t* block_table,
+                                   const int32_t* seq_lens, const int32_t* sel, const int32_t* n_sel, void* out,
+                                   float* out_lse, int B, int Hq, int Hkv, int D, int num_pages, int page_size, int W,
+                                   int K, size_t q_stride_b, size_t q_stride_h, size_t stride_page,
+                                   size_t stride_token, size_t stride_head, size_t table_stride, float scale,
+                                   int dtype, int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!aligned(q, 16) || !aligned(v_pool, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(out, 16))
+    return RING_EINVAL;
+  if (out_lse && !aligned(out_lse, 4)) return RING_EINVAL;
+  if ((sel == nullptr) != (n_sel == nullptr)) return RING_EINVAL;
+  if (sel && (!aligned(sel, 4) || !aligned(n_sel, 4) || K < 1)) return RING_EINVAL;
+  if (B < 1 || Hq < 1 || Hkv < 1 || W < 1 || page_size < 1 || Hq % Hkv || table_stride < (size_t)W) return RING_EINVAL;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return RING_EINVAL;
+  if (!good_dtype(out_dtype)) return RING_EINVAL;
+  const int pl = page_log2(page_size);
+  if (pl < 0) return RING_EUNSUPPORTED;
+  PagedDecodeArgs a{};
+  const ring_status rs = pool_check(k_pool, num_pages, pl, Hkv, D, stride_page, stride_token, stride_head, dtype,
+                                    &a.pool);
+  if (rs != RING_OK) return rs;
+  if (dtype == RING_FP32 && out_dtype != RING_FP32) return RING_EUNSUPPORTED;
+  const int eb = elem_bytes(dtype);
+  if (!good_rows(q_stride_b, q_stride_h, B, Hq, D, eb)) return RING_EINVAL;
+  if (!table_fits(W, pl) || table_stride >= (size_t(1) << 32) || (sel && !table_fits(K, pl))) return RING_EINVAL;
+  // tiles of the call are counted in 32 bits (a segment is a kv head's group of at most 16 query heads, or 8)
+  const long long keys = (long long)(sel ? K : W) << pl;
+  const long long segs = (long long)B * Hkv * ((Hq / Hkv + 7) / 8);
+  if (segs * ((keys + kPagedTile - 1) / kPagedTile) > 0x7fffffffLL || (long long)B * Hq * D > 0x7fffffffLL)
+    return RING_EINVAL;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < paged_decode_workspace_bytes(D))
+    return RING_EINVAL;
+  a.q = q; a.k = k_pool; a.v = v_pool; a.table = block_table; a.seq_lens = seq_lens; a.sel = sel; a.n_sel = n_sel;
+  a.out = out; a.out_lse = out_lse;
+  paged_decode_workspace_split(workspace, D, &a.ws_part, &a.ws_count);
+  a.q_b = (long long)q_stride_b;
+  a.q_h = (long long)q_stride_h;
+  a.table_stride = (long long)table_stride;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.num_pages = num_pages; a.ps_log2 = pl; a.W = W; a.K = sel ? K : 0;
+  a.G = Hq / Hkv;
+  a.scale = scale;
+  a.out_fp32 = out_dtype == RING_FP32;
+  a.err = error_word();
+  return from_cuda(launch_paged_decode_simt(a, dtype == RING_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ring_status ring_attn_page_bounds(const void* k_pool, void* bounds, const int32_t* block_table,
+                                  const int32_t* seq_lens, const int32_t* start_lens, int B, int Hkv, int D,
+                                  int num_pages, int page_size, int W, size_t stride_page, size_t stride_token,
+                                  size_t stride_head, size_t table_stride, int dtype, void* stream) {
+  if (!aligned(bounds, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4)) return RING_EINVAL;
+  if (start_lens && !aligned(start_lens, 4)) return RING_EINVAL;
+  if (B < 1 || W < 1 || page_size < 1 || table_stride < (size_t)W) return RING_EINVAL;
+  const int pl = page_log2(page_size);
+  if (pl < 0 || B > 65535) return RING_EUNSUPPORTED;
+  BoundsArgs a{};
+  const ring_status rs = pool_check(k_pool, num_pages, pl, Hkv, D, stride_page, stride_token, stride_head, dtype,
+                                    &a.pool);
+  if (rs != RING_OK) return rs;
+  if (!table_fits(W, pl) || table_stride >= (size_t(1) << 32)) return RING_EINVAL;
+  a.k = k_pool; a.bounds = bounds; a.table = block_table; a.seq_lens = seq_lens; a.start_lens = start_lens;
+  a.table_stride = (long long)table_stride;
+  a.B = B; a.Hkv = Hkv; a.D = D; a.num_pages = num_pages; a.ps_log2 = pl; a.W = W; a.elem_bytes = elem_bytes(dtype);
+  return from_cuda(launch_page_bounds(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ring_status ring_attn_page_scores(const void* q, const void* bounds, const int32_t* block_table,
+                                  const int32_t* seq_lens, float* scores, int B, int Hq, int Hkv, int D, int num_pages,
+                                  int page_size, int W, size_t q_stride_b, size_t q_stride_h, size_t table_stride,
+                                  int dtype, void* stream) {
+  if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(scores, 4))
+    return RING_EINVAL;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || D < 1 || W < 1 || num_pages < 1 || page_size < 1 ||
+      table_stride < (size_t)W || !good_dtype(dtype))
+    return RING_EINVAL;
+  const int pl = page_log2(page_size);
+  if (pl < 0 || (D != 64 && D != 128) || (long long)B * Hkv > 65535) return RING_EUNSUPPORTED;
+  if (Hq / Hkv > 64) return RING_EUNSUPPORTED;    // the group's queries sit in shared memory
+  const int eb = elem_bytes(dtype);
+  if (!good_rows(q_stride_b, q_stride_h, B, Hq, D, eb)) return RING_EINVAL;
+  if (!table_fits(W, pl) || !table_fits(num_pages, pl) || table_stride >= (size_t(1) << 32)) return RING_EINVAL;
+  ScoresArgs a{};
+  a.q = q; a.bounds = bounds; a.table = block_table; a.seq_lens = seq_lens; a.scores = scores;
+  a.q_b = (long long)q_stride_b;
+  a.q_h = (long long)q_stride_h;
+  a.table_stride = (long long)table_stride;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.num_pages = num_pages; a.ps_log2 = pl; a.W = W;
+  return from_cuda(launch_page_scores(a, dtype == RING_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ring_status ring_attn_page_select(const float* scores, const int32_t* seq_lens, int32_t* sel, int32_t* n_sel, int B,
+                                  int Hkv, int W, int page_size, int K, int keep_first, int keep_last, void* stream) {
+  if (!aligned(scores, 4) || !aligned(seq_lens, 4) || !aligned(sel, 4) || !aligned(n_sel, 4)) return RING_EINVAL;
+  if (B < 1 || Hkv < 1 || W < 1 || K < 1 || page_size < 1 || keep_first < 0 || keep_last < 0 ||
+      (long long)keep_first + keep_last > K)
+    return RING_EINVAL;
+  const int pl = page_log2(page_size);
+  if (pl < 0) return RING_EUNSUPPORTED;
+  if (!table_fits(W, pl) || (long long)B * Hkv > 0x7fffffffLL) return RING_EINVAL;
+  SelectArgs a{scores, seq_lens, sel, n_sel, B, Hkv, W, pl, K, keep_first, keep_last};
+  return from_cuda(launch_page_select(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

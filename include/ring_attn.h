@@ -54,7 +54,7 @@ typedef enum {
   RING_EUNSUPPORTED = -2,  /* valid but not built: head dim, dtype combination */
   RING_ECUDA = -3,         /* a CUDA runtime / driver call or a launch failed */
   RING_ETIMEOUT = -4,      /* a bounded wait inside a kernel expired */
-  RING_ECAPACITY = -5      /* a KV append found its shard full (see ring_attn_kv_append) */
+  RING_ECAPACITY = -5      /* a KV append found its shard full, or a page extend its free list empty */
 } ring_status;
 
 /*
@@ -417,6 +417,183 @@ ring_status ring_attn_kv_append(void* k_cache, void* v_cache, const void* k_new,
                                 int D, int P, int block, int dtype, void* stream);
 
 /*
+ * A paged KV cache.  A cache page holds page_size tokens (a power of two,
+ * RING_PAGE_MIN .. RING_PAGE_MAX; another size is RING_EUNSUPPORTED).  The
+ * pools k_pool, v_pool are [num_pages, page_size, Hkv, D] with D contiguous
+ * and the same strides (in elements, multiples of 16 bytes) stride_page,
+ * stride_token, stride_head, so that K and V may be interleaved and heads may
+ * come before tokens.  block_table[b*table_stride + i], i < W, is the pool
+ * page of tokens [i*page_size, (i+1)*page_size) of sequence b; seq_lens[b]
+ * tokens are valid.  All index arrays are int32 on the device, and every
+ * entry point below reads them there, so that a captured launch follows them;
+ * lengths are clamped to [0, W*page_size], a table entry outside
+ * [0, num_pages) marks its tokens as absent, and nothing outside the caller's
+ * buffers is touched whatever the arrays hold.  (The source pages shard a
+ * contiguous cache; the paged layout is this library's.)
+ */
+#define RING_PAGE_MIN 8
+#define RING_PAGE_MAX 1024
+
+/*
+ * ring_attn_page_extend -- pages and cache rows ("slots") for new tokens.
+ *
+ * Sequence b grows from seq_lens[b] by new_lens[b] (< 0 counts as 0) tokens.
+ * Pages come from the end of the free list free_pages[0 .. n_free[0]), in
+ * order of sequence and page, and are entered in block_table.  Written:
+ *   cu_new [B+1]      prefix sums of new_lens: the call's tokens, packed,
+ *                     are numbered cu_new[b] .. cu_new[b+1]-1 in sequence b
+ *   start_lens [B]    the length before the call, or -1 (see below)
+ *   slot_map [max_tokens]  token t's cache row, page*page_size + offset; -1
+ *                     for the numbers from cu_new[B] on and for the tokens of
+ *                     a sequence that was left as it was
+ *   seq_lens, n_free  advanced.
+ * A sequence is left as it was (start_lens -1) if its new length exceeds
+ * W*page_size, if its tokens pass max_tokens, or if the free list does not
+ * hold its pages after those of the sequences before it (a sequence that
+ * needs no new page is served all the same); ring_attn_device_error() then
+ * reports RING_ECAPACITY.  Entries of block_table that are not taken into use
+ * keep their value.  The page numbers themselves are not checked here.
+ * Returns RING_EINVAL for null/misaligned pointers, sizes < 1, table_stride <
+ * W or W*page_size beyond 32 bits; RING_EUNSUPPORTED for a page size that is
+ * not built; RING_ECUDA on launch failure.
+ * The source pages have no counterpart.
+ */
+ring_status ring_attn_page_extend(int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table,
+                                  const int32_t* free_pages, int32_t* n_free, int32_t* slot_map,
+                                  int32_t* start_lens, int32_t* cu_new, int B, int W, size_t table_stride,
+                                  int page_size, int max_free, int max_tokens, void* stream);
+
+/*
+ * ring_attn_page_trim -- shorten sequences and give their pages back.
+ *
+ * Sequence b is cut to keep_lens[b] tokens (clamped to [0, seq_lens[b]]: 0
+ * ends the sequence, seq_lens[b] leaves it).  The pages past the new ends go
+ * onto the free list, the last of the last sequence first, so that extending
+ * by some tokens and cutting the same tokens off again restores the list.
+ * free_pages has room for max_free pages; what would pass that is dropped and
+ * ring_attn_device_error() reports RING_ECAPACITY.  block_table is not
+ * changed.  Errors as ring_attn_page_extend.
+ * The source pages have no counterpart.
+ */
+ring_status ring_attn_page_trim(int32_t* seq_lens, const int32_t* keep_lens, const int32_t* block_table,
+                                int32_t* free_pages, int32_t* n_free, int B, int W, size_t table_stride,
+                                int page_size, int max_free, void* stream);
+
+/*
+ * ring_attn_paged_append -- write K and V rows into their cache pages.
+ *
+ * Row t of k_new, v_new [T, Hkv, D] (strides new_token, new_head in elements,
+ * multiples of 16 bytes: slices of a fused projection will do) goes to row
+ * slot_map[t] of the pools.  A slot outside [0, num_pages*page_size), -1 for
+ * instance, is skipped; of rows with the same slot one is kept, which one (or
+ * a mixture of them) is not said.
+ * Returns RING_EINVAL for null/misaligned pointers, sizes < 1, strides that
+ * are not multiples of 16 bytes or shorter than a row, or a pool of more than
+ * 2^31 rows; RING_EUNSUPPORTED unless D is 64 or 128, or for a page size that
+ * is not built; RING_ECUDA on launch failure.
+ * "NVIDIA unveils Helix Parallelism" grows a contiguous cache
+ * (ring_attn_kv_append); this is the paged cache's write.
+ */
+ring_status ring_attn_paged_append(void* k_pool, void* v_pool, const void* k_new, const void* v_new,
+                                   const int32_t* slot_map, int T, int Hkv, int D, int num_pages, int page_size,
+                                   size_t stride_page, size_t stride_token, size_t stride_head, size_t new_token,
+                                   size_t new_head, int dtype, void* stream);
+
+/* Bytes of workspace ring_attn_decode_paged needs (0 on bad sizes: D other than 64 or 128).
+ * A library helper; the source pages have no counterpart. */
+size_t ring_attn_decode_paged_workspace_bytes(int D);
+
+/*
+ * ring_attn_decode_paged -- attention of one new token per sequence over a
+ * paged cache, split over the keys and joined in one launch (the (O, lse)
+ * merge of ring_attn_merge inside the kernel).
+ *
+ * q [B,Hq,D] of dtype (strides q_stride_b, q_stride_h in elements); query head
+ * h reads kv head h / (Hq / Hkv), for any Hq / Hkv.  out [B,Hq,D] of
+ * out_dtype (RING_BF16 or RING_FP32 for a bf16 cache, RING_FP32 for a float32
+ * one), out_lse [B,Hq] float (may be NULL): attention over the seq_lens[b]
+ * keys of sequence b, or, with sel [B,Hkv,K] and n_sel [B,Hkv] (both or
+ * neither NULL), over those of them that lie in the pages listed for the kv
+ * head: sel holds indices into the sequence's row of block_table, of which
+ * the first n_sel (clamped to [0, K]) count; indices outside the sequence add
+ * nothing, and a page listed twice counts twice.  A row without a key gives
+ * out = 0, lse = -inf.  Keys past the length may hold anything.
+ * The float32 out with out_lse of a shard of a sequence can be merged with
+ * other shards' by ring_attn_merge.
+ * workspace: ring_attn_decode_paged_workspace_bytes(D) bytes, 256-byte
+ * aligned; its counters must be zero before the first call on it and every
+ * call that completes leaves them zero (after RING_ETIMEOUT, zero it again).
+ * Calls that share a workspace must not overlap on the GPU.
+ *
+ * Returns RING_EINVAL for null/misaligned pointers, sizes < 1, Hq % Hkv != 0,
+ * only one of sel / n_sel, bad strides, scale or dtype, a workspace too small
+ * or sizes beyond 32-bit counts of tiles; RING_EUNSUPPORTED unless D is 64 or
+ * 128, for a page size that is not built, or for a bf16 out of a float32
+ * cache; RING_ECUDA on launch failure.
+ * The split-KV decode of "NVIDIA unveils Helix Parallelism", Phase 1, over a
+ * paged cache.
+ */
+ring_status ring_attn_decode_paged(const void* q, const void* k_pool, const void* v_pool,
+                                   const int32_t* block_table, const int32_t* seq_lens, const int32_t* sel,
+                                   const int32_t* n_sel, void* out, float* out_lse, int B, int Hq, int Hkv, int D,
+                                   int num_pages, int page_size, int W, int K, size_t q_stride_b, size_t q_stride_h,
+                                   size_t stride_page, size_t stride_token, size_t stride_head, size_t table_stride,
+                                   float scale, int dtype, int out_dtype, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * ring_attn_page_bounds -- per page and kv head, the elementwise minimum and
+ * maximum of the page's valid keys.
+ *
+ * bounds [num_pages, Hkv, 2, D] of dtype: [.., 0, :] the minimum, [.., 1, :]
+ * the maximum (a NaN among the keys makes both NaN).  Written for the pages of
+ * each sequence that hold tokens from start_lens[b] on (from 0 if start_lens
+ * is NULL, as after a prompt; < 0 counts as 0), over all valid keys of the
+ * page; the other pages' bounds are not touched.  A page that two sequences
+ * share must be full in both.
+ * Errors as ring_attn_paged_append, plus RING_EUNSUPPORTED for B > 65535.
+ * The source pages have no counterpart.
+ */
+ring_status ring_attn_page_bounds(const void* k_pool, void* bounds, const int32_t* block_table,
+                                  const int32_t* seq_lens, const int32_t* start_lens, int B, int Hkv, int D,
+                                  int num_pages, int page_size, int W, size_t stride_page, size_t stride_token,
+                                  size_t stride_head, size_t table_stride, int dtype, void* stream);
+
+/*
+ * ring_attn_page_scores -- an upper bound of every page's largest score.
+ *
+ * scores [B,Hkv,W] float: for page i of sequence b and kv head g, with
+ * (lo, hi) the bounds of its pool page, the largest over the query heads h of
+ * the group of sum_d max(q[b,h,d] lo_d, q[b,h,d] hi_d): no key of the page has
+ * a larger q . k.  -inf from the sequence's last page on and for table entries
+ * outside the pool.  q as in ring_attn_decode_paged.
+ * Errors as ring_attn_page_bounds, plus RING_EUNSUPPORTED for Hq / Hkv > 64
+ * or B * Hkv > 65535.
+ * The source pages have no counterpart.
+ */
+ring_status ring_attn_page_scores(const void* q, const void* bounds, const int32_t* block_table,
+                                  const int32_t* seq_lens, float* scores, int B, int Hq, int Hkv, int D,
+                                  int num_pages, int page_size, int W, size_t q_stride_b, size_t q_stride_h,
+                                  size_t table_stride, int dtype, void* stream);
+
+/*
+ * ring_attn_page_select -- the K best pages per (sequence, kv head).
+ *
+ * Of the np = ceil(seq_lens[b] / page_size) pages of sequence b: the first
+ * keep_first and the last keep_last, and then those of the largest scores
+ * [B,Hkv,W] (a NaN counts as the largest, -0 as 0; of equal scores the lower
+ * index), min(np, K) in all.  sel [B,Hkv,K] receives their indices in
+ * ascending order, then -1; n_sel [B,Hkv] their number: the lists of
+ * ring_attn_decode_paged.
+ * Returns RING_EINVAL for null/misaligned pointers, sizes < 1, keep_first or
+ * keep_last < 0 or together above K; RING_EUNSUPPORTED for a page size that is
+ * not built; RING_ECUDA on launch failure.
+ * The source pages have no counterpart.
+ */
+ring_status ring_attn_page_select(const float* scores, const int32_t* seq_lens, int32_t* sel, int32_t* n_sel, int B,
+                                  int Hkv, int W, int page_size, int K, int keep_first, int keep_last, void* stream);
+
+/*
  * ring_attn_sched_stats -- the scheduler's host-side view of one (batch, head)
  * of a causal or full ring, without running anything: per-rank unmasked
  * chunk pairs (a diagonal pair counts once; "Lesson 8", section 4B: 2P+1 per
@@ -436,7 +613,8 @@ ring_status ring_attn_sched_stats(int S, int P, int causal, int layout, int tile
  * ring_attn_device_error -- synchronise the current device and read-and-clear
  * the library's device error word.  Returns RING_ETIMEOUT if a bounded wait
  * in any kernel expired since the last call, RING_ECAPACITY if a KV append
- * dropped a token because its shard was full, RING_ECUDA if the device
+ * dropped a token because its shard was full or ring_attn_page_extend /
+ * _page_trim ran out of room, RING_ECUDA if the device
  * reports an error, else RING_OK.  `where` (may be NULL) receives the code
  * of the site that recorded the error (0 if none).  Code 12 (reported as
  * RING_ETIMEOUT: the kernel unwound without results) means a CTA pair of the
