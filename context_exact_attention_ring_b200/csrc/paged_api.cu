@@ -171,7 +171,8 @@ ring_status ring_attn_decode_paged(const void* q, const void* k_pool, const void
   a.scale = scale;
   a.out_fp32 = out_dtype == RING_FP32;
   a.err = error_word();
-  return from_cuda(launch_paged_decode_simt(a, dtype == RING_BF16, reinterpret_cast<cudaStream_t>(stream)));
+  cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+  return from_cuda(dtype == RING_BF16 ? launch_paged_decode(a, strm) : launch_paged_decode_simt(a, strm));
 }
 
 ring_status ring_attn_page_bounds(const void* k_pool, void* bounds, const int32_t* block_table,

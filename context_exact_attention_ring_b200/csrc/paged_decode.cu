@@ -1,0 +1,559 @@
+// Paged decode on the tensor cores (bf16 cache): one new token per sequence
+// against the keys in its cache pages, in one pass with a running maximum and
+// sum, split over the keys and joined in the same launch (paged_split.cuh).
+//
+// The query heads of a kv head share every K/V row, so a 128-key tile is a
+// pair of small tcgen05 products, heads padded to 16 columns:
+//   S^T = K Q^T       M = 128 keys, N = 16 heads, K = D   (K, Q K-major)
+//   O^T += V^T P^T    M = 128 dims, N = 2 x 8 or 2 x 16, K = 128 keys
+// N = 16 is the narrowest product, so 8 heads leave half of its columns
+// empty: the weights go in as two bf16 terms, p = hi + lo with |p - hi - lo|
+// <= 2^-16 p, in columns of their own, and the output is float32-accurate up
+// to its own rounding for the price of the second shared-memory store.
+//
+// Bound by HBM: a tile is 64 KB at D = 128 against 2 x 128 x 16 x D products.
+// One CTA per SM; warp roles:
+//   warps 0-3  softmax: thread t owns tensor-memory lane t (key row t of S^T,
+//              dim t of O^T);
+//   warp 4     producer: lane i owns page slot i of a tile (a tile holds
+//              128 / page_size pages, or is part of one).  It looks the page
+//              up one tile ahead and issues the page's TMA boxes into a ring
+//              of 3 stages, next to the page's number of valid keys;
+//   warp 5     MMA issuer and tensor-memory owner.  Tiles follow each other
+//              across segments without a drain: S^T(t+1) is issued before
+//              O^T(t), and Q, O^T and the weights have two buffers.
+// A key that is not valid (past the length, or in an absent page) has weight 0
+// and its V row is zeroed in shared memory, whatever the page held there.
+// Every wait is bounded.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "kernels.h"
+#include "paged.h"
+#include "paged_split.cuh"
+#include "ptx.cuh"
+
+namespace ra {
+
+namespace pdt {
+constexpr int NQ = 16;                      // heads per CTA, padded
+constexpr int NST = 3;                      // K/V stages
+constexpr int SLAB = kPagedTile * 128;      // 128 rows x 64 columns of bf16 (16 KB)
+constexpr int TILE_BYTES = 2 * SLAB;        // one K or V tile
+constexpr int QSLAB = NQ * 128;
+constexpr int CT = 128;                     // softmax threads
+constexpr int THREADS = CT + 64;
+constexpr uint32_t TMEM_COLS = 128;         // S^T 2 x 16, O^T 2 x (16 or 32)
+constexpr float LAZY = 8.f;                 // log2 of the growth tolerated before the base moves
+constexpr int MAX_SLOTS = kPagedTile / 8;   // page slots of a tile
+constexpr int MIN_TILES = 2;                // fewest tiles worth a CTA
+}  // namespace pdt
+
+template <int GP>
+struct PagedSmem {
+  static constexpr int NP = 2 * GP;           // weight columns: hi, lo
+  static constexpr int PSLAB = NP * 128;      // 64 keys of all weight columns
+  alignas(1024) uint8_t kv[pdt::NST][2][pdt::TILE_BYTES];
+  alignas(1024) uint8_t q[2][2 * pdt::QSLAB];
+  alignas(1024) uint8_t pt[2][2 * PSLAB];
+  int nvalid[pdt::NST][pdt::MAX_SLOTS];       // valid keys per page slot
+  float red[2][4][GP];                        // cross-warp maxima, by tile parity
+  float suml[4][GP];
+  alignas(8) uint64_t kv_full[pdt::NST], kv_empty[pdt::NST];
+  alignas(8) uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], o_done[2], o_full[2], o_free[2], teardown;
+  PagedRunSmem run;
+  uint32_t tmem_base;
+  int is_last, abort_flag;
+};
+
+struct PagedMaps {
+  int head_outer;     // the pools' head stride is the larger: box order (D, token, head, page)
+  int q_rows;         // rows of a query box
+};
+
+__host__ __device__ constexpr uint32_t paged_idesc(int N, bool a_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+
+// N consecutive 32-bit columns of this warp's lanes, N = 1, 2, 4, 8, 16
+template <int N>
+__device__ __forceinline__ void paged_tmem_ld(uint32_t t, float (&v)[N]) {
+  uint32_t r[N];
+  if constexpr (N == 1)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(t));
+  else if constexpr (N == 2)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(t));
+  else if constexpr (N == 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(t));
+  else if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t));
+  else
+    tmem_ld16(t, r);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+template <int N>
+__device__ __forceinline__ void paged_tmem_st(uint32_t t, const float (&v)[N]) {
+  uint32_t r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = __float_as_uint(v[i]);
+  if constexpr (N == 1)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(t), "r"(r[0]) : "memory");
+  else if constexpr (N == 2)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(t), "r"(r[0]), "r"(r[1]) : "memory");
+  else if constexpr (N == 4)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(t), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]) : "memory");
+  else if constexpr (N == 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+  else
+    tmem_st16(t, r);
+}
+
+template <int G, int DH>
+__global__ void __launch_bounds__(pdt::THREADS, 1)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, PagedDecodeArgs a, PagedMaps maps) {
+  using namespace pdt;
+  constexpr int GP = G <= 8 ? 8 : 16;
+  using Smem = PagedSmem<GP>;
+  constexpr int NP = Smem::NP, PSLAB = Smem::PSLAB;
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sm.abort_flag;
+  unsigned int* err = a.err;
+  const PagedRows rows = paged_rows(a);
+  const int psn_log2 = min(a.ps_log2, 7), psn = 1 << psn_log2;   // rows of a page slot
+
+  // padded query rows and weight columns stay zero
+  {
+    uint4* z = reinterpret_cast<uint4*>(&sm.q[0][0]);
+    constexpr int n16 = (int)((sizeof(sm.q) + sizeof(sm.pt)) / 16);
+    for (int i = threadIdx.x; i < n16; i += THREADS) z[i] = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (DH == 64)
+      // the second 64 columns of V: the upper half of M = 128 dims, zero
+      for (int st = 0; st < NST; ++st) {
+        uint4* zv = reinterpret_cast<uint4*>(sm.kv[st][1] + SLAB);
+        for (int i = threadIdx.x; i < SLAB / 16; i += THREADS) zv[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    fence_proxy_async_smem();
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(smem_u32(&sm.kv_full[s]), 1);
+      mbar_init(smem_u32(&sm.kv_empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.q_full[i]), 1);
+      mbar_init(smem_u32(&sm.q_empty[i]), 1);
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.s_free[i]), CT);
+      mbar_init(smem_u32(&sm.p_full[i]), CT);
+      mbar_init(smem_u32(&sm.o_done[i]), 1);
+      mbar_init(smem_u32(&sm.o_full[i]), 1);
+      mbar_init(smem_u32(&sm.o_free[i]), CT);
+    }
+    mbar_init(smem_u32(&sm.teardown), 1);
+    sm.abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  const PagedRun run = paged_run<THREADS>(a, sm.run, MIN_TILES);   // synchronises the CTA
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    const uint64_t pol_kv = l2_policy_evict_first(), pol_q = l2_policy_evict_last();
+    const int nslots = kPagedTile >> psn_log2;
+    PagedWalk walk(run);
+    PagedPiece pc;
+    uint32_t cnt = 0, nq = 0;
+    bool ok = true;
+    while (ok && walk.next(a, rows, pc)) {
+      const PagedHead hd = paged_head(a, pc.row, pc.sub, NQ);
+      const int len = paged_len(a, hd.b);
+      const int qb = nq & 1;
+      if (nq >= 2) ok = mbar_wait(smem_u32(&sm.q_empty[qb]), ((nq >> 1) - 1) & 1u, abort_flag, kWaitQEmpty, err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        const uint32_t qf = smem_u32(&sm.q_full[qb]);
+        mbar_arrive_expect_tx(qf, (uint32_t)maps.q_rows * DH * 2);
+        for (int sl = 0; sl < DH / 64; ++sl)
+          tma_load_4d(smem_u32(sm.q[qb]) + sl * QSLAB, &tmQ, qf, sl * 64, hd.h0, hd.b, 0, pol_q);
+      }
+      ++nq;
+      auto span = [&](int j) {
+        PagedSpan s;
+        s.valid = 0;
+        s.page = s.in_page = 0;
+        if (lane < nslots) s = paged_span(a, hd.b, hd.g, len, j * kPagedTile + (lane << psn_log2), psn);
+        return s;
+      };
+      PagedSpan next = span(pc.a);
+      for (int j = pc.a; j < pc.b; ++j) {
+        const PagedSpan cur = next;
+        if (j + 1 < pc.b) next = span(j + 1);
+        const int s = cnt % NST;
+        ok = mbar_wait(smem_u32(&sm.kv_empty[s]), ((cnt / NST) & 1u) ^ 1u, abort_flag, kWaitDecodeEmpty, err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const bool live = cur.valid > 0;
+        const uint32_t npages = __popc(__ballot_sync(0xffffffffu, live));
+        if (lane < MAX_SLOTS) sm.nvalid[s][lane] = cur.valid;
+        __syncwarp();
+        const uint32_t fb = smem_u32(&sm.kv_full[s]);
+        if (lane == 0) mbar_arrive_expect_tx(fb, npages * (uint32_t)(2 * DH * 2) << psn_log2);
+        __syncwarp();
+        if (live) {
+          const int c1 = maps.head_outer ? cur.in_page : hd.g, c2 = maps.head_outer ? hd.g : cur.in_page;
+          const uint32_t dst = (uint32_t)lane << (psn_log2 + 7);
+#pragma unroll
+          for (int sl = 0; sl < DH / 64; ++sl) {
+            tma_load_4d(smem_u32(sm.kv[s][0]) + sl * SLAB + dst, &tmK, fb, sl * 64, c1, c2, cur.page, pol_kv);
+            tma_load_4d(smem_u32(sm.kv[s][1]) + sl * SLAB + dst, &tmV, fb, sl * 64, c1, c2, cur.page, pol_kv);
+          }
+        }
+        ++cnt;
+      }
+    }
+    // do not leave while copies are still landing in shared memory
+    if (lane == 0) {
+      for (uint32_t c = (cnt > (uint32_t)NST ? cnt - NST : 0); c < cnt; ++c)
+        mbar_wait(smem_u32(&sm.kv_full[c % NST]), (c / NST) & 1u, nullptr, kWaitTeardown, err);
+      for (uint32_t c = (nq > 2u ? nq - 2u : 0u); c < nq; ++c)
+        mbar_wait(smem_u32(&sm.q_full[c & 1]), (c >> 1) & 1u, nullptr, kWaitTeardown, err);
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idS = paged_idesc(NQ, false), idPV = paged_idesc(NP, true);
+      PagedWalk walk(run);
+      PagedPiece pc;
+      uint32_t t = 0, nu = 0;
+      bool ok = true;
+      bool prev_first = false, prev_last = false;
+      uint32_t prev_u = 0;
+      // O^T += V^T P^T of tile tt
+      auto pv = [&](uint32_t tt) -> bool {
+        const uint32_t s = tt % NST, pb = tt & 1u, ob = prev_u & 1u;
+        if (!mbar_wait(smem_u32(&sm.p_full[pb]), (tt >> 1) & 1u, abort_flag, kWaitPFull, err)) return false;
+        if (prev_first && prev_u >= 2 &&
+            !mbar_wait(smem_u32(&sm.o_free[ob]), ((prev_u >> 1) - 1) & 1u, abort_flag, kWaitOFinal, err))
+          return false;
+        tc_fence_after();
+        const uint64_t vdesc = sw128_desc(smem_u32(sm.kv[s][1]), SLAB, 1024);
+        const uint64_t pdesc = sw128_desc(smem_u32(sm.pt[pb]), 16, 1024);
+        const uint32_t tO = tmem + 32 + ob * NP;
+#pragma unroll
+        for (int k = 0; k < kPagedTile / 16; ++k)
+          mma_ss(tO, vdesc + ((k * 16 * 128) >> 4), pdesc + ((((k >> 2) * PSLAB) + (k & 3) * 32) >> 4), idPV,
+                 (!prev_first || k > 0) ? 1u : 0u);
+        mma_commit(smem_u32(&sm.o_done[pb]));
+        mma_commit(smem_u32(&sm.kv_empty[s]));
+        if (prev_last) mma_commit(smem_u32(&sm.o_full[ob]));
+        return true;
+      };
+      while (ok && walk.next(a, rows, pc)) {
+        const int qb = nu & 1;
+        if (!mbar_wait(smem_u32(&sm.q_full[qb]), (nu >> 1) & 1u, abort_flag, kWaitQFull, err)) { ok = false; break; }
+        const uint64_t qdesc = sw128_desc(smem_u32(sm.q[qb]), 16, 1024);
+        for (int j = pc.a; j < pc.b && ok; ++j) {
+          const uint32_t s = t % NST, sb = t & 1u;
+          if (!mbar_wait(smem_u32(&sm.kv_full[s]), (t / NST) & 1u, abort_flag, kWaitDecodeFull, err) ||
+              (t >= 2 && !mbar_wait(smem_u32(&sm.s_free[sb]), ((t >> 1) - 1) & 1u, abort_flag, kWaitSFull, err))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t kdesc = sw128_desc(smem_u32(sm.kv[s][0]), 16, 1024);
+#pragma unroll
+          for (int k = 0; k < DH / 16; ++k)
+            mma_ss(tmem + 16 * sb, kdesc + ((((k >> 2) * SLAB) + (k & 3) * 32) >> 4),
+                   qdesc + ((((k >> 2) * QSLAB) + (k & 3) * 32) >> 4), idS, k > 0 ? 1u : 0u);
+          mma_commit(smem_u32(&sm.s_full[sb]));
+          if (j == pc.b - 1) mma_commit(smem_u32(&sm.q_empty[qb]));
+          if (t > 0) ok = pv(t - 1);
+          prev_first = j == pc.a;
+          prev_last = j == pc.b - 1;
+          prev_u = nu;
+          ++t;
+        }
+        ++nu;
+      }
+      if (ok && t > 0) pv(t - 1);
+      // every product issued so far must be complete before tensor memory is freed
+      mma_commit(smem_u32(&sm.teardown));
+      mbar_wait(smem_u32(&sm.teardown), 0, nullptr, kWaitTeardown, err);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int row = threadIdx.x;                              // key row of S^T, dim of O^T
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const float sl2 = a.scale * 1.4426950408889634f;
+    const int slot = row >> psn_log2, in_slot = row & (psn - 1);
+    // this thread's key in the weight operand: 16-byte chunk kc (XOR row) of 64-key slab row >> 6
+    const uint32_t pt_base = (uint32_t)((row >> 6) * PSLAB + (row & 7) * 2);
+    const int kc = (row & 63) >> 3;
+    paged_empty_rows(a, row, CT);
+    PagedWalk walk(run);
+    PagedPiece pc;
+    uint32_t t = 0, nu = 0;
+    bool ok = true;
+    while (ok && walk.next(a, rows, pc)) {
+      const PagedHead hd = paged_head(a, pc.row, pc.sub, NQ);
+      float m[G], l[G];      // per head: base (the same in every thread), this thread's sum
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        m[h] = -CUDART_INF_F;
+        l[h] = 0.f;
+      }
+      for (int j = pc.a; j < pc.b; ++j, ++t) {
+        const uint32_t sb = t & 1u, st = t % NST;
+        // the stage's valid counts, the scores, and a weight buffer that O^T has taken
+        bool good = mbar_wait(smem_u32(&sm.kv_full[st]), (t / NST) & 1u, abort_flag, kWaitDecodeFull, err);
+        if (good) good = mbar_wait(smem_u32(&sm.s_full[sb]), (t >> 1) & 1u, abort_flag, kWaitSFull, err);
+        if (good && t >= 2)
+          good = mbar_wait(smem_u32(&sm.o_done[sb]), ((t >> 1) - 1) & 1u, abort_flag, kWaitPFull, err);
+        __syncwarp();
+        tc_fence_after();
+        float xs[G];
+        paged_tmem_ld<G>(tmem + lane_off + 16 * sb, xs);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sm.s_free[sb]));
+        const bool valid = in_slot < sm.nvalid[st][slot];
+        if (!valid) {
+          uint4* vr = reinterpret_cast<uint4*>(sm.kv[st][1] + row * 128);
+#pragma unroll
+          for (int sl = 0; sl < DH / 64; ++sl)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) vr[sl * (SLAB / 16) + c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        bool exceed = false;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          xs[h] = valid ? xs[h] * sl2 : -CUDART_INF_F;
+          exceed |= xs[h] > m[h] + LAZY;
+        }
+        if (named_bar_any(1, CT, exceed || !good)) {
+          if (named_bar_any(1, CT, !good)) {
+            ok = false;
+            break;
+          }
+          // move the base of the heads whose tile maximum exceeds it (always on a piece's first tile)
+          const int rb = t & 1;
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            float mw = xs[h];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
+            if (lane == 0) sm.red[rb][warp][h] = mw;
+          }
+          named_bar_sync(1, CT);
+          float alpha[G];
+          bool moved = false;
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float mt = fmaxf(fmaxf(sm.red[rb][0][h], sm.red[rb][1][h]), fmaxf(sm.red[rb][2][h], sm.red[rb][3][h]));
+            alpha[h] = 1.f;
+            if (mt > m[h] + LAZY) {
+              alpha[h] = m[h] == -CUDART_INF_F ? 0.f : ex2(m[h] - mt);
+              m[h] = mt;
+              moved = true;
+            }
+            l[h] *= alpha[h];
+          }
+          if (j > pc.a && moved) {
+            // rescale O^T once it holds the piece's earlier tiles; the same decision in every thread
+            const uint32_t tp = t - 1;
+            good = mbar_wait(smem_u32(&sm.o_done[tp & 1u]), (tp >> 1) & 1u, abort_flag, kWaitPFull, err);
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t tO = tmem + lane_off + 32 + (nu & 1u) * NP;
+            float o[G];
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              paged_tmem_ld<G>(tO + part * GP, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int h = 0; h < G; ++h) o[h] *= alpha[h];
+              paged_tmem_st<G>(tO + part * GP, o);
+            }
+            tmem_wait_st();
+            if (named_bar_any(1, CT, !good)) {
+              ok = false;
+              break;
+            }
+          }
+        }
+        // weights against the base, as two bf16 terms, for the tensor cores
+        uint8_t* ptb = sm.pt[sb] + pt_base;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          const float pw = xs[h] == -CUDART_INF_F ? 0.f : ex2(xs[h] - m[h]);
+          l[h] += pw;
+          const uint32_t hi = pack_bf16x2(pw, 0.f) & 0xffffu;
+          const uint32_t lo = pack_bf16x2(pw - __uint_as_float(hi << 16), 0.f);
+          constexpr int lo_off = (GP >> 3) * 1024;     // GP rows further down
+          uint8_t* at = ptb + (h >> 3) * 1024 + (h & 7) * 128 + ((kc ^ (h & 7)) << 4);
+          *reinterpret_cast<uint16_t*>(at) = (uint16_t)hi;
+          *reinterpret_cast<uint16_t*>(at + lo_off) = (uint16_t)lo;
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sm.p_full[sb]));
+      }
+      if (!ok) break;
+
+      // ---- the piece's result
+      const bool fin = mbar_wait(smem_u32(&sm.o_full[nu & 1u]), (nu >> 1) & 1u, abort_flag, kWaitOFinal, err);
+      __syncwarp();
+      tc_fence_after();
+      float o[G], olo[G];
+      const uint32_t tO = tmem + lane_off + 32 + (nu & 1u) * NP;
+      paged_tmem_ld<G>(tO, o);
+      paged_tmem_ld<G>(tO + GP, olo);
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sm.o_free[nu & 1u]));
+      ++nu;
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        float s = l[h];
+#pragma unroll
+        for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        if (lane == 0) sm.suml[warp][h] = s;
+      }
+      if (named_bar_any(1, CT, !fin)) {
+        ok = false;
+        break;
+      }
+      const bool whole = pc.a == 0 && pc.b == pc.nt;
+      float* part = paged_part(a, run, blockIdx.x, pc.seg_t);
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        if (h >= hd.nh) continue;
+        const float L = (sm.suml[0][h] + sm.suml[1][h]) + (sm.suml[2][h] + sm.suml[3][h]);
+        const float od = L == 0.f ? 0.f : (o[h] + olo[h]) / L;
+        const float lse = L == 0.f ? -CUDART_INF_F : (m[h] + log2f(L)) * 0.6931471805599453f;
+        if (row >= DH) continue;      // D = 64: the upper half of O^T is padding
+        if (whole) {
+          const size_t bh = (size_t)hd.b * a.Hq + hd.h0 + h;
+          paged_store(a, bh * DH + row, od);
+          if (row == 0 && a.out_lse) a.out_lse[bh] = lse;
+        } else {
+          part[h * DH + row] = od;
+          if (row == 0) part[kPagedHeads * DH + h] = lse;
+        }
+      }
+      if (!whole) {
+        const int c0 = run_owner(run.T, run.n, pc.seg_t), c1 = run_owner(run.T, run.n, pc.seg_t + pc.nt - 1);
+        named_bar_sync(1, CT);      // the part is written
+        if (row == 0) {
+          const unsigned int old = atom_add_acq_rel_gpu(a.ws_count + c0, 1u);
+          sm.is_last = old == (unsigned int)(c1 - c0);
+          if (sm.is_last) atomicExch(a.ws_count + c0, 0u);    // zero again for the next call
+        }
+        named_bar_sync(1, CT);
+        if (sm.is_last) paged_join<CT>(a, run, pc, hd, c0, c1, row);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// 4-D bf16 map: innermost D (boxes of 64, 128-byte swizzle), then three
+// dimensions with strides in elements and box sizes.
+static bool paged_map(CUtensorMap* m, const void* base, int D, const long long (&dim)[3], const long long (&stride)[3],
+                      const int (&box)[3]) {
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)dim[0], (cuuint64_t)dim[1], (cuuint64_t)dim[2]};
+  cuuint64_t strides[3];
+  for (int i = 0; i < 3; ++i) strides[i] = (cuuint64_t)(dim[i] > 1 ? stride[i] : D) * 2;   // of one entry: any will do
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)box[0], (cuuint32_t)box[1], (cuuint32_t)box[2]};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxes, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int G, int DH>
+static cudaError_t launch_paged_tc(const PagedDecodeArgs& a, cudaStream_t st) {
+  CUtensorMap tq, tk, tv;
+  PagedMaps maps;
+  maps.head_outer = a.pool.head > a.pool.token;
+  maps.q_rows = a.G < pdt::NQ ? a.G : pdt::NQ;
+  const int ps = 1 << a.ps_log2, rows = ps < kPagedTile ? ps : kPagedTile;
+  if (!paged_map(&tq, a.q, DH, {a.Hq, a.B, 1}, {a.q_h, a.q_b, a.q_b}, {maps.q_rows, 1, 1})) return cudaErrorInvalidValue;
+  const PoolStrides& p = a.pool;
+  for (int i = 0; i < 2; ++i) {
+    const void* base = i ? a.v : a.k;
+    CUtensorMap* m = i ? &tv : &tk;
+    if (!(maps.head_outer
+              ? paged_map(m, base, DH, {ps, a.Hkv, a.num_pages}, {p.token, p.head, p.page}, {rows, 1, 1})
+              : paged_map(m, base, DH, {a.Hkv, ps, a.num_pages}, {p.head, p.token, p.page}, {1, rows, 1})))
+      return cudaErrorInvalidValue;
+  }
+  const size_t smem = sizeof(PagedSmem<(G <= 8 ? 8 : 16)>) + 1024;
+  auto kern = paged_decode_kernel<G, DH>;
+  // the shared-memory limit is raised once per device
+  static std::atomic<unsigned long long> raised{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(raised.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int grid = num_sms() < kPagedMaxCtas ? num_sms() : kPagedMaxCtas;
+  kern<<<grid, pdt::THREADS, smem, st>>>(tq, tk, tv, a, maps);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_decode(const PagedDecodeArgs& args, cudaStream_t st) {
+  PagedDecodeArgs a = args;
+  a.ngrp = (a.G + pdt::NQ - 1) / pdt::NQ;
+  auto pick = [&](auto d) -> cudaError_t {
+    constexpr int DD = decltype(d)::value;
+    if (a.G == 1) return launch_paged_tc<1, DD>(a, st);
+    if (a.G == 2) return launch_paged_tc<2, DD>(a, st);
+    if (a.G <= 4) return launch_paged_tc<4, DD>(a, st);
+    if (a.G <= 8) return launch_paged_tc<8, DD>(a, st);
+    return launch_paged_tc<16, DD>(a, st);
+  };
+  return a.D == 64 ? pick(std::integral_constant<int, 64>{}) : pick(std::integral_constant<int, 128>{});
+}
+
+}  // namespace ra

@@ -8,9 +8,7 @@
 // (paged_split.cuh) 128 keys at a time, 16 keys a warp: 16 lanes share a key
 // row, so that a row is one contiguous load of the half-warp, and each lane
 // keeps D/16 dims of the queries and outputs of up to 8 heads in registers.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <type_traits>
 
 #include "kernels.h"
 #include "paged.h"
@@ -26,12 +24,10 @@ constexpr int HEADS = 8;    // query heads of a group, at most
 }  // namespace pds
 static_assert(pds::NW * 2 * pds::KPW == kPagedTile, "a CTA takes a tile at a time");
 
-// Dims of a row that lane l (0..15) of a half-warp holds, as D/64 pieces of 4
-// (float32) or D/128 pieces of 8 / D/64 of 4 (bf16): contiguous over lanes.
-template <typename T, int D>
-struct RowPiece;
+// Dims of a row that lane l (0..15) of a half-warp holds: D/64 pieces of 4,
+// contiguous over the lanes.
 template <int D>
-struct RowPiece<float, D> {
+struct RowPiece {
   static constexpr int N = D / 16;
   __device__ __forceinline__ static int dim(int l, int i) { return (i >> 2) * 64 + l * 4 + (i & 3); }
   __device__ __forceinline__ static void load(const float* row, int l, float (&x)[N]) {
@@ -39,26 +35,6 @@ struct RowPiece<float, D> {
     for (int j = 0; j < N / 4; ++j) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(row + j * 64 + l * 4));
       x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
-    }
-  }
-};
-template <int D>
-struct RowPiece<__nv_bfloat16, D> {
-  static constexpr int N = D / 16;
-  __device__ __forceinline__ static int dim(int l, int i) { return l * N + i; }
-  __device__ __forceinline__ static void load(const __nv_bfloat16* row, int l, float (&x)[N]) {
-    uint32_t w[N / 2];
-    if constexpr (N == 8) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + l * 8));
-      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + l * 4));
-      w[0] = v.x; w[1] = v.y;
-    }
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
 };
@@ -71,10 +47,10 @@ struct SimtSmem {
   int last;
 };
 
-template <typename T, int G, int D>
+template <int G, int D>
 __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(PagedDecodeArgs a) {
   using namespace pds;
-  using Row = RowPiece<T, D>;
+  using Row = RowPiece<D>;
   constexpr int N = Row::N;
   __shared__ SimtSmem<G, D> sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = lane >> 4, l16 = lane & 15;
@@ -90,7 +66,7 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
     float q[G][N], acc[G][N], m[G], l[G];
 #pragma unroll
     for (int h = 0; h < G; ++h) {
-      const T* qr = static_cast<const T*>(a.q) + (size_t)hd.b * a.q_b + (size_t)(hd.h0 + (h < hd.nh ? h : 0)) * a.q_h;
+      const float* qr = static_cast<const float*>(a.q) + (size_t)hd.b * a.q_b + (size_t)(hd.h0 + (h < hd.nh ? h : 0)) * a.q_h;
       Row::load(qr, l16, q[h]);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -106,8 +82,8 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
       const PagedSpan sp = paged_span(a, hd.b, hd.g, len, k0, KPW);
       const size_t base = (size_t)max(sp.page, 0) * a.pool.page + (size_t)sp.in_page * a.pool.token +
                           (size_t)hd.g * a.pool.head;
-      const T* kr = static_cast<const T*>(a.k) + base;
-      const T* vr = static_cast<const T*>(a.v) + base;
+      const float* kr = static_cast<const float*>(a.k) + base;
+      const float* vr = static_cast<const float*>(a.v) + base;
 #pragma unroll
       for (int u0 = 0; u0 < KPW; u0 += 4) {
         float kx[4][N], vx[4][N], s[4][G];
@@ -210,27 +186,23 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
   }
 }
 
-template <typename T, int G>
+template <int G>
 static cudaError_t launch_simt(const PagedDecodeArgs& a, cudaStream_t st) {
   const int grid = min(num_sms(), kPagedMaxCtas);
   if (a.D == 64)
-    paged_decode_simt_kernel<T, G, 64><<<grid, pds::THREADS, 0, st>>>(a);
+    paged_decode_simt_kernel<G, 64><<<grid, pds::THREADS, 0, st>>>(a);
   else
-    paged_decode_simt_kernel<T, G, 128><<<grid, pds::THREADS, 0, st>>>(a);
+    paged_decode_simt_kernel<G, 128><<<grid, pds::THREADS, 0, st>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_paged_decode_simt(const PagedDecodeArgs& args, bool bf16, cudaStream_t st) {
+cudaError_t launch_paged_decode_simt(const PagedDecodeArgs& args, cudaStream_t st) {
   PagedDecodeArgs a = args;
   a.ngrp = (a.G + pds::HEADS - 1) / pds::HEADS;
-  auto pick = [&](auto t) -> cudaError_t {
-    using T = decltype(t);
-    if (a.G == 1) return launch_simt<T, 1>(a, st);
-    if (a.G == 2) return launch_simt<T, 2>(a, st);
-    if (a.G <= 4) return launch_simt<T, 4>(a, st);
-    return launch_simt<T, 8>(a, st);
-  };
-  return bf16 ? pick(__nv_bfloat16{}) : pick(float{});
+  if (a.G == 1) return launch_simt<1>(a, st);
+  if (a.G == 2) return launch_simt<2>(a, st);
+  if (a.G <= 4) return launch_simt<4>(a, st);
+  return launch_simt<8>(a, st);
 }
 
 static size_t part_bytes(int D) {
