@@ -50,11 +50,13 @@ constexpr int THREADS = CT + 64;
 constexpr uint32_t TMEM_COLS = 128;         // S^T 2 x 16, O^T 2 x (16 or 32)
 constexpr float LAZY = 8.f;                 // log2 of the growth tolerated before the base moves
 constexpr int MAX_SLOTS = kPagedTile / 8;   // page slots of a tile
-constexpr int MIN_TILES = 2;                // fewest tiles worth a CTA
+constexpr int SEG_COST = 1;                 // what a segment costs besides its tiles, in tiles
+constexpr int PARTS_PER_TILE = 10;          // parts joined in the time of a tile
 }  // namespace pdt
 
-template <int GP>
+template <int G, int DH>
 struct PagedSmem {
+  static constexpr int GP = G <= 8 ? 8 : 16;  // weight columns of a term
   static constexpr int NP = 2 * GP;           // weight columns: hi, lo
   static constexpr int PSLAB = NP * 128;      // 64 keys of all weight columns
   alignas(1024) uint8_t kv[pdt::NST][2][pdt::TILE_BYTES];
@@ -62,7 +64,8 @@ struct PagedSmem {
   alignas(1024) uint8_t pt[2][2 * PSLAB];
   int nvalid[pdt::NST][pdt::MAX_SLOTS];       // valid keys per page slot
   float red[2][4][GP];                        // cross-warp maxima, by tile parity
-  float suml[4][GP];
+  float suml[2][4][GP], base[2][GP];          // cross-warp sums and final bases, by piece parity
+  alignas(16) typename PagedJoin<pdt::CT, G, DH>::Smem join;
   alignas(8) uint64_t kv_full[pdt::NST], kv_empty[pdt::NST];
   alignas(8) uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], o_done[2], o_full[2], o_free[2], teardown;
   PagedRunSmem run;
@@ -118,14 +121,20 @@ __device__ __forceinline__ void paged_tmem_st(uint32_t t, const float (&v)[N]) {
     tmem_st16(t, r);
 }
 
+// Maximum over the warp's lanes (NaN ignored, as fmaxf does).
+__device__ __forceinline__ float warp_max_redux(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 template <int G, int DH>
 __global__ void __launch_bounds__(pdt::THREADS, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, PagedDecodeArgs a, PagedMaps maps) {
   using namespace pdt;
-  constexpr int GP = G <= 8 ? 8 : 16;
-  using Smem = PagedSmem<GP>;
-  constexpr int NP = Smem::NP, PSLAB = Smem::PSLAB;
+  using Smem = PagedSmem<G, DH>;
+  constexpr int GP = Smem::GP, NP = Smem::NP, PSLAB = Smem::PSLAB;
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -172,7 +181,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const PagedRun run = paged_run<THREADS>(a, sm.run, MIN_TILES);   // synchronises the CTA
+  const PagedRun run = paged_run<THREADS>(a, sm.run, SEG_COST, PARTS_PER_TILE);   // synchronises the CTA
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
@@ -186,7 +195,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     }
     const uint64_t pol_kv = l2_policy_evict_first(), pol_q = l2_policy_evict_last();
     const int nslots = kPagedTile >> psn_log2;
-    PagedWalk walk(run);
+    PagedWalk walk(run, SEG_COST);
     PagedPiece pc;
     uint32_t cnt = 0, nq = 0;
     bool ok = true;
@@ -249,7 +258,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idS = paged_idesc(NQ, false), idPV = paged_idesc(NP, true);
-      PagedWalk walk(run);
+      PagedWalk walk(run, SEG_COST);
       PagedPiece pc;
       uint32_t t = 0, nu = 0;
       bool ok = true;
@@ -317,12 +326,70 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     const uint32_t pt_base = (uint32_t)((row >> 6) * PSLAB + (row & 7) * 2);
     const int kc = (row & 63) >> 3;
     paged_empty_rows(a, row, CT);
-    PagedWalk walk(run);
+    // the piece whose products are all issued, to be finished while the next one's run
+    PagedPiece fpc{};
+    PagedHead fhd{};
+    float fl[G];
+    uint32_t fu = 0;
+    auto finish = [&]() -> bool {
+      const uint32_t ob = fu & 1u;
+      const bool fin = mbar_wait(smem_u32(&sm.o_full[ob]), (fu >> 1) & 1u, abort_flag, kWaitOFinal, err);
+      __syncwarp();
+      tc_fence_after();
+      float o[G], olo[G];
+      const uint32_t tO = tmem + lane_off + 32 + ob * NP;
+      paged_tmem_ld<G>(tO, o);
+      paged_tmem_ld<G>(tO + GP, olo);
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sm.o_free[ob]));
+      ++fu;
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        float s = fl[h];
+#pragma unroll
+        for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        if (lane == 0) sm.suml[ob][warp][h] = s;
+      }
+      if (named_bar_any(1, CT, !fin)) return false;
+      const bool whole = fpc.a == 0 && fpc.b == fpc.nt;
+      float* part = paged_part(a, blockIdx.x, run.t0 >= fpc.seg_t ? 0 : 1);
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        if (h >= fhd.nh) continue;
+        const float L = (sm.suml[ob][0][h] + sm.suml[ob][1][h]) + (sm.suml[ob][2][h] + sm.suml[ob][3][h]);
+        const float od = L == 0.f ? 0.f : (o[h] + olo[h]) / L;
+        const float lse = L == 0.f ? -CUDART_INF_F : (sm.base[ob][h] + log2f(L)) * 0.6931471805599453f;
+        if (row >= DH) continue;      // D = 64: the upper half of O^T is padding
+        if (whole) {
+          const size_t bh = (size_t)fhd.b * a.Hq + fhd.h0 + h;
+          paged_store(a, bh * DH + row, od);
+          if (row == 0 && a.out_lse) a.out_lse[bh] = lse;
+        } else {
+          part[h * DH + row] = od;
+          if (row == 0) part[kPagedHeads * DH + h] = lse;
+        }
+      }
+      if (!whole) {
+        const int c0 = run_owner(run.T, run.n, fpc.seg_t), c1 = run_owner(run.T, run.n, fpc.seg_t + fpc.nt - 1);
+        named_bar_sync(1, CT);      // the part is written
+        if (row == 0) {
+          const unsigned int old = atom_add_acq_rel_gpu(a.ws_count + c0, 1u);
+          sm.is_last = old == (unsigned int)(c1 - c0);
+          if (sm.is_last) atomicExch(a.ws_count + c0, 0u);    // zero again for the next call
+        }
+        named_bar_sync(1, CT);
+        if (sm.is_last)
+          paged_join<CT, G, DH>(a, run, fpc, fhd, c0, c1, row, sm.join, [] { named_bar_sync(1, CT); });
+      }
+      return true;
+    };
+
+    PagedWalk walk(run, SEG_COST);
     PagedPiece pc;
     uint32_t t = 0, nu = 0;
     bool ok = true;
     while (ok && walk.next(a, rows, pc)) {
-      const PagedHead hd = paged_head(a, pc.row, pc.sub, NQ);
       float m[G], l[G];      // per head: base (the same in every thread), this thread's sum
 #pragma unroll
       for (int h = 0; h < G; ++h) {
@@ -357,21 +424,18 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
           xs[h] = valid ? xs[h] * sl2 : -CUDART_INF_F;
           exceed |= xs[h] > m[h] + LAZY;
         }
-        if (named_bar_any(1, CT, exceed || !good)) {
+        // a piece's first tile always sets the bases; later ones only where a score exceeds one
+        if (j == pc.a || named_bar_any(1, CT, exceed || !good)) {
+          const int rb = t & 1;
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float mw = warp_max_redux(xs[h]);
+            if (lane == 0) sm.red[rb][warp][h] = mw;
+          }
           if (named_bar_any(1, CT, !good)) {
             ok = false;
             break;
           }
-          // move the base of the heads whose tile maximum exceeds it (always on a piece's first tile)
-          const int rb = t & 1;
-#pragma unroll
-          for (int h = 0; h < G; ++h) {
-            float mw = xs[h];
-#pragma unroll
-            for (int o = 16; o; o >>= 1) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
-            if (lane == 0) sm.red[rb][warp][h] = mw;
-          }
-          named_bar_sync(1, CT);
           float alpha[G];
           bool moved = false;
 #pragma unroll
@@ -424,62 +488,22 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.p_full[sb]));
+        if (j == pc.a && nu > 0 && !finish()) {
+          ok = false;
+          break;
+        }
       }
       if (!ok) break;
-
-      // ---- the piece's result
-      const bool fin = mbar_wait(smem_u32(&sm.o_full[nu & 1u]), (nu >> 1) & 1u, abort_flag, kWaitOFinal, err);
-      __syncwarp();
-      tc_fence_after();
-      float o[G], olo[G];
-      const uint32_t tO = tmem + lane_off + 32 + (nu & 1u) * NP;
-      paged_tmem_ld<G>(tO, o);
-      paged_tmem_ld<G>(tO + GP, olo);
-      tmem_wait_ld();
-      tc_fence_before();
-      mbar_arrive(smem_u32(&sm.o_free[nu & 1u]));
+      fpc = pc;
+      fhd = paged_head(a, pc.row, pc.sub, NQ);
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        if (row == 0) sm.base[nu & 1u][h] = m[h];
+        fl[h] = l[h];
+      }
       ++nu;
-#pragma unroll
-      for (int h = 0; h < G; ++h) {
-        float s = l[h];
-#pragma unroll
-        for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        if (lane == 0) sm.suml[warp][h] = s;
-      }
-      if (named_bar_any(1, CT, !fin)) {
-        ok = false;
-        break;
-      }
-      const bool whole = pc.a == 0 && pc.b == pc.nt;
-      float* part = paged_part(a, run, blockIdx.x, pc.seg_t);
-#pragma unroll
-      for (int h = 0; h < G; ++h) {
-        if (h >= hd.nh) continue;
-        const float L = (sm.suml[0][h] + sm.suml[1][h]) + (sm.suml[2][h] + sm.suml[3][h]);
-        const float od = L == 0.f ? 0.f : (o[h] + olo[h]) / L;
-        const float lse = L == 0.f ? -CUDART_INF_F : (m[h] + log2f(L)) * 0.6931471805599453f;
-        if (row >= DH) continue;      // D = 64: the upper half of O^T is padding
-        if (whole) {
-          const size_t bh = (size_t)hd.b * a.Hq + hd.h0 + h;
-          paged_store(a, bh * DH + row, od);
-          if (row == 0 && a.out_lse) a.out_lse[bh] = lse;
-        } else {
-          part[h * DH + row] = od;
-          if (row == 0) part[kPagedHeads * DH + h] = lse;
-        }
-      }
-      if (!whole) {
-        const int c0 = run_owner(run.T, run.n, pc.seg_t), c1 = run_owner(run.T, run.n, pc.seg_t + pc.nt - 1);
-        named_bar_sync(1, CT);      // the part is written
-        if (row == 0) {
-          const unsigned int old = atom_add_acq_rel_gpu(a.ws_count + c0, 1u);
-          sm.is_last = old == (unsigned int)(c1 - c0);
-          if (sm.is_last) atomicExch(a.ws_count + c0, 0u);    // zero again for the next call
-        }
-        named_bar_sync(1, CT);
-        if (sm.is_last) paged_join<CT>(a, run, pc, hd, c0, c1, row);
-      }
     }
+    if (ok && nu > 0) finish();
   }
 
   tc_fence_before();
@@ -524,7 +548,8 @@ static cudaError_t launch_paged_tc(const PagedDecodeArgs& a, cudaStream_t st) {
               : paged_map(m, base, DH, {a.Hkv, ps, a.num_pages}, {p.head, p.token, p.page}, {1, rows, 1})))
       return cudaErrorInvalidValue;
   }
-  const size_t smem = sizeof(PagedSmem<(G <= 8 ? 8 : 16)>) + 1024;
+  const size_t smem = sizeof(PagedSmem<G, DH>) + 1024;
+  static_assert(sizeof(PagedSmem<G, DH>) + 1024 <= 232448, "shared memory of a CTA");
   auto kern = paged_decode_kernel<G, DH>;
   // the shared-memory limit is raised once per device
   static std::atomic<unsigned long long> raised{0};

@@ -21,6 +21,8 @@ constexpr int THREADS = 256;
 constexpr int NW = THREADS / 32;
 constexpr int KPW = 8;      // keys a half-warp holds at once (a tile is 8 warps x 2 x 8 keys)
 constexpr int HEADS = 8;    // query heads of a group, at most
+constexpr int SEG_COST = 1;         // what a segment costs besides its tiles, in tiles
+constexpr int PARTS_PER_TILE = 10;  // parts joined in the time of a tile
 }  // namespace pds
 static_assert(pds::NW * 2 * pds::KPW == kPagedTile, "a CTA takes a tile at a time");
 
@@ -42,7 +44,10 @@ struct RowPiece {
 template <int G, int D>
 struct SimtSmem {
   PagedRunSmem run;
-  float o[pds::NW][G][D];
+  union {
+    float o[pds::NW][G][D];
+    typename PagedJoin<pds::THREADS, G, D>::Smem join;
+  };
   float m[pds::NW][G], l[pds::NW][G];
   int last;
 };
@@ -55,10 +60,10 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
   __shared__ SimtSmem<G, D> sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = lane >> 4, l16 = lane & 15;
   const PagedRows rows = paged_rows(a);
-  const PagedRun run = paged_run<THREADS>(a, sm.run, 2);
+  const PagedRun run = paged_run<THREADS>(a, sm.run, SEG_COST, PARTS_PER_TILE);
   paged_empty_rows(a, tid, THREADS);
   const float sl2 = a.scale * 1.4426950408889634f;
-  PagedWalk walk(run);
+  PagedWalk walk(run, SEG_COST);
   PagedPiece pc;
   while (walk.next(a, rows, pc)) {
     const PagedHead hd = paged_head(a, pc.row, pc.sub, HEADS);
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
     }
     __syncthreads();
     const bool whole = pc.a == 0 && pc.b == pc.nt;
-    float* part = paged_part(a, run, blockIdx.x, pc.seg_t);
+    float* part = paged_part(a, blockIdx.x, run.t0 >= pc.seg_t ? 0 : 1);
     for (int e = tid; e < hd.nh * D; e += THREADS) {
       const int h = e / D, d = e - h * D;
       float mx = -CUDART_INF_F;
@@ -181,7 +186,8 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
         if (sm.last) atomicExch(a.ws_count + c0, 0u);    // zero again for the next call
       }
       __syncthreads();
-      if (sm.last) paged_join<THREADS>(a, run, pc, hd, c0, c1, tid);
+      if (sm.last)
+        paged_join<THREADS, G, D>(a, run, pc, hd, c0, c1, tid, sm.join, [] { __syncthreads(); });
     }
   }
 }

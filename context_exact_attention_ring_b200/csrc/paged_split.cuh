@@ -2,8 +2,8 @@
 //
 // The keys of every (sequence, kv head, head group) -- a segment -- are cut
 // into tiles of 128, and all tiles of the call, segment after segment, are
-// dealt to n CTAs in n equal contiguous runs (CTA c gets tiles
-// [cT/n, (c+1)T/n) of T).  Ragged batches balance whatever their lengths, one
+// dealt to n CTAs in n equal contiguous runs (CTA c gets units
+// [cT/n, (c+1)T/n) of T, where a unit is a tile or a segment's fixed cost).  Ragged batches balance whatever their lengths, one
 // long sequence spreads over the whole GPU, and the lengths are read on the
 // device, so a captured launch follows them.  A run covers whole segments,
 // whose result is written at once, and at most two parts of segments (at its
@@ -41,41 +41,62 @@ __device__ __forceinline__ int paged_tiles(const PagedDecodeArgs& a, int r) {
   return (paged_keys(a, r) + kPagedTile - 1) / kPagedTile;
 }
 
+// Units of work of a row's segments: its tiles, and what starting and
+// finishing a segment costs, in tiles (a run's boundary in that tail belongs
+// to no tile).
+__device__ __forceinline__ int paged_units(int tiles, int seg_cost) { return tiles ? tiles + seg_cost : 0; }
+
 struct PagedRun {
-  int T;          // tiles of the call
+  int T;          // units of the call
   int n;          // CTAs that have work
-  int t0, t1;     // this CTA's tiles
+  int t0, t1;     // this CTA's units
   int row;        // row that holds t0
-  int row_t;      // first tile of that row
+  int row_t;      // first unit of that row
 };
 __device__ __forceinline__ int run_start(int T, int n, int c) { return (int)((long long)c * T / n); }
 __device__ __forceinline__ int run_owner(int T, int n, int t) { return (int)(((long long)(t + 1) * n - 1) / T); }
 
 struct PagedRunSmem {
-  int warp_sum[32];
-  int row, row_t, total;
+  int warp_sum[32], warp_rows[32];
+  int row, row_t;
 };
 
-// All threads of the CTA (a multiple of 32, at most 1024).  min_tiles: the
-// fewest tiles worth a CTA of their own.
+// All threads of the CTA (a multiple of 32, at most 1024).
+// parts_per_tile: how many parts a segment may be cut into for every tile of
+// a part.  Joining takes as long as a tile for every parts_per_tile parts, so
+// that cutting n parts of T / n tiles is longest at n^2 = parts_per_tile T.
 template <int kThreads>
-__device__ __forceinline__ PagedRun paged_run(const PagedDecodeArgs& a, PagedRunSmem& s, int min_tiles) {
+__device__ __forceinline__ PagedRun paged_run(const PagedDecodeArgs& a, PagedRunSmem& s, int seg_cost,
+                                              int parts_per_tile) {
   constexpr int NW = kThreads / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedRows rows = paged_rows(a);
-  // total number of tiles; the first kThreads rows stay in registers
+  // all tiles and all rows with keys; the first kThreads rows stay in registers
   const int mine = tid < rows.R ? paged_tiles(a, tid) : 0;
-  int sum = mine;
-  for (int r = tid + kThreads; r < rows.R; r += kThreads) sum += paged_tiles(a, r);
+  int sum = mine, some = mine > 0;
+  for (int r = tid + kThreads; r < rows.R; r += kThreads) {
+    const int nt = paged_tiles(a, r);
+    sum += nt;
+    some += nt > 0;
+  }
   sum = __reduce_add_sync(0xffffffffu, sum);
-  if (lane == 0) s.warp_sum[warp] = sum;
+  some = __reduce_add_sync(0xffffffffu, some);
+  if (lane == 0) {
+    s.warp_sum[warp] = sum;
+    s.warp_rows[warp] = some;
+  }
   __syncthreads();
-  int total = 0;
+  int tiles = 0, segs = 0;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) total += s.warp_sum[w];
+  for (int w = 0; w < NW; ++w) {
+    tiles += s.warp_sum[w];
+    segs += s.warp_rows[w];
+  }
   PagedRun run;
-  run.T = total * rows.mult;
-  run.n = min((int)gridDim.x, max(1, run.T / min_tiles));
+  run.T = (tiles + segs * seg_cost) * rows.mult;
+  tiles *= rows.mult;
+  segs *= rows.mult;
+  run.n = max(1, min(min((int)gridDim.x, tiles), (int)sqrtf((float)parts_per_tile * tiles * segs)));
   run.row = run.row_t = 0;
   const int c = blockIdx.x;
   if (run.T == 0 || c >= run.n) {
@@ -85,12 +106,12 @@ __device__ __forceinline__ PagedRun paged_run(const PagedDecodeArgs& a, PagedRun
   run.t0 = run_start(run.T, run.n, c);
   run.t1 = run_start(run.T, run.n, c + 1);
   // the row that holds t0
-  const int want = run.t0 / rows.mult;    // tile index counted once per row
+  const int want = run.t0 / rows.mult;    // units counted once per row
   int base = 0;
   for (int r0 = 0; r0 < rows.R; r0 += kThreads) {
     const int r = r0 + tid;
-    const int nt = r0 == 0 ? mine : (r < rows.R ? paged_tiles(a, r) : 0);
-    int incl = nt;
+    const int nu = paged_units(r0 == 0 ? mine : (r < rows.R ? paged_tiles(a, r) : 0), seg_cost);
+    int incl = nu;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, incl, o);
@@ -105,7 +126,7 @@ __device__ __forceinline__ PagedRun paged_run(const PagedDecodeArgs& a, PagedRun
       if (w < warp) before += s.warp_sum[w];
       chunk += s.warp_sum[w];
     }
-    const int hi = before + incl, lo = hi - nt;
+    const int hi = before + incl, lo = hi - nu;
     if (lo <= want && want < hi) {
       s.row = r;
       s.row_t = lo * rows.mult;
@@ -124,28 +145,33 @@ struct PagedPiece {
   int row, sub;    // row and segment of the row
   int nt;          // tiles of the whole segment
   int a, b;        // this piece's tiles
-  int seg_t;       // first tile of the segment, counted over the call
+  int seg_t;       // first unit of the segment, counted over the call
 };
 struct PagedWalk {
-  int t, t1, row, row_t;
-  __device__ __forceinline__ explicit PagedWalk(const PagedRun& r) : t(r.t0), t1(r.t1), row(r.row), row_t(r.row_t) {}
+  int t, t1, row, row_t, seg_cost;
+  __device__ __forceinline__ PagedWalk(const PagedRun& r, int cost)
+      : t(r.t0), t1(r.t1), row(r.row), row_t(r.row_t), seg_cost(cost) {}
   __device__ __forceinline__ bool next(const PagedDecodeArgs& a, const PagedRows& rows, PagedPiece& p) {
-    if (t >= t1) return false;
-    int nt = paged_tiles(a, row);
-    while (t - row_t >= nt * rows.mult) {    // never past the last row: t < t1 <= T
-      row_t += nt * rows.mult;
-      ++row;
-      nt = paged_tiles(a, row);
+    while (t < t1) {
+      int nt = paged_tiles(a, row), nu = paged_units(nt, seg_cost);
+      while (t - row_t >= nu * rows.mult) {    // never past the last row: t < t1 <= T
+        row_t += nu * rows.mult;
+        ++row;
+        nt = paged_tiles(a, row);
+        nu = paged_units(nt, seg_cost);
+      }
+      const int o = t - row_t;
+      p.row = row;
+      p.sub = o / nu;
+      p.nt = nt;
+      p.a = o - p.sub * nu;
+      const int end = min(nu, p.a + (t1 - t));
+      p.b = min(nt, end);
+      p.seg_t = row_t + p.sub * nu;
+      t += end - p.a;
+      if (p.a < p.b) return true;    // else only the tail of a segment
     }
-    const int o = t - row_t;
-    p.row = row;
-    p.sub = o / nt;
-    p.nt = nt;
-    p.a = o - p.sub * nt;
-    p.b = min(nt, p.a + (t1 - t));
-    p.seg_t = row_t + p.sub * nt;
-    t += p.b - p.a;
-    return true;
+    return false;
   }
 };
 // Sequence, kv head and first query head (of the call's Hq) of a piece.
@@ -217,34 +243,118 @@ __device__ __forceinline__ void paged_empty_rows(const PagedDecodeArgs& a, int t
   }
 }
 
-// Workspace slot of CTA c's part of the segment that starts at tile seg_t:
-// slot 0 if the CTA's run starts inside the segment (or with it), else 1.
-__device__ __forceinline__ float* paged_part(const PagedDecodeArgs& a, const PagedRun& run, int c, int seg_t) {
-  const int slot = run_start(run.T, run.n, c) >= seg_t ? 0 : 1;
+// Workspace slot of this CTA's part of the segment that starts at tile seg_t:
+// 0 if its run starts inside the segment (or with it), else 1.  Only the
+// first CTA of a segment can have started before it.
+__device__ __forceinline__ float* paged_part(const PagedDecodeArgs& a, int c, int slot) {
   return a.ws_part + (size_t)(c * 2 + slot) * kPagedHeads * (a.D + 1);
 }
 
-// Joins the parts of a segment (its CTAs c0..c1) and writes the result.
-// Called by kThreads threads after the acquire of the last arrival.
-template <int kThreads>
+// Joins the parts of a segment (of its CTAs c0..c1) and writes the result, 8
+// heads at a time.  Called by kThreads threads after the acquire of the last
+// arrival; sync() is their barrier.  First a warp takes a head's lse values, a
+// lane every 32nd, all loaded at once, and leaves the weights in shared
+// memory.  Then D / 4 lanes to a row add the parts up, 4 dims each: the groups
+// of lanes share out the heads first and then the parts, and their 16-byte
+// loads wait for nothing but the weights.  (One thread per output looking the
+// parts up one after the other took 60 us of a 65 us call.)
+template <int kThreads, int G, int D>
+struct PagedJoin {
+  static constexpr int H = G < 8 ? G : 8;                       // heads at a time
+  static constexpr int NG = kThreads / (D / 4);                 // groups of lanes
+  static constexpr int HS = H < NG ? H : NG, PS = NG / HS;      // groups over heads, over parts
+  static constexpr int HPG = H / HS;                            // heads of a group
+  struct Smem {
+    float w[kPagedMaxCtas * H];
+    alignas(16) float o[PS > 1 ? PS * H * D : 4];               // sums of the groups over parts
+  };
+};
+template <int kThreads, int G, int D, typename Sync>
 __device__ __forceinline__ void paged_join(const PagedDecodeArgs& a, const PagedRun& run, const PagedPiece& pc,
-                                           const PagedHead& hd, int c0, int c1, int tid) {
-  for (int e = tid; e < hd.nh * a.D; e += kThreads) {
-    const int h = e / a.D, d = e - h * a.D;
-    float mx = -CUDART_INF_F;
-    for (int c = c0; c <= c1; ++c)
-      mx = fmaxf(mx, __ldcg(paged_part(a, run, c, pc.seg_t) + kPagedHeads * a.D + h));
-    float L = 0.f, acc = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const float* part = paged_part(a, run, c, pc.seg_t);
-      const float lse = __ldcg(part + kPagedHeads * a.D + h);
-      const float w = lse == -CUDART_INF_F ? 0.f : expf(lse - mx);   // a part without a key adds nothing
-      L += w;
-      acc = fmaf(w, __ldcg(part + h * a.D + d), acc);
+                                           const PagedHead& hd, int c0, int c1, int tid,
+                                           typename PagedJoin<kThreads, G, D>::Smem& js, Sync sync) {
+  using J = PagedJoin<kThreads, G, D>;
+  constexpr int NW = kThreads / 32;
+  constexpr int KV = (kPagedMaxCtas + 31) / 32;                 // lse values per lane
+  const int warp = tid >> 5, lane = tid & 31;
+  const int n = c1 - c0 + 1;
+  const int slot0 = run_start(run.T, run.n, c0) >= pc.seg_t ? 0 : 1;
+  const int step = 2 * kPagedHeads * (D + 1);
+  const float* first = paged_part(a, c0, slot0);
+  const float* rest = paged_part(a, c0, 0);                     // part i > 0 at rest + i step
+  const size_t bh0 = (size_t)hd.b * a.Hq + hd.h0;
+  const int d4 = tid % (D / 4), grp = tid / (D / 4);
+  for (int hb = 0; hb < hd.nh; hb += J::H) {
+    for (int h = warp; h < J::H && hb + h < hd.nh; h += NW) {
+      float w[KV], mx = -CUDART_INF_F;
+#pragma unroll
+      for (int k = 0; k < KV; ++k) {
+        const int c = lane + 32 * k;
+        w[k] = c < n ? __ldcg((c ? rest + c * step : first) + kPagedHeads * D + hb + h) : -CUDART_INF_F;
+      }
+#pragma unroll
+      for (int k = 0; k < KV; ++k) mx = fmaxf(mx, w[k]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      float L = 0.f;
+#pragma unroll
+      for (int k = 0; k < KV; ++k) {
+        w[k] = w[k] == -CUDART_INF_F ? 0.f : expf(w[k] - mx);   // a part without a key adds nothing
+        L += w[k];
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+      for (int k = 0; k < KV; ++k)
+        if (lane + 32 * k < n) js.w[(lane + 32 * k) * J::H + h] = w[k] * inv;
+      if (lane == 0 && a.out_lse) a.out_lse[bh0 + hb + h] = L == 0.f ? -CUDART_INF_F : mx + logf(L);
     }
-    const size_t bh = (size_t)hd.b * a.Hq + hd.h0 + h;
-    paged_store(a, bh * a.D + d, L == 0.f ? 0.f : acc / L);
-    if (d == 0 && a.out_lse) a.out_lse[bh] = L == 0.f ? -CUDART_INF_F : mx + logf(L);
+    sync();
+    const int hg = (grp % J::HS) * J::HPG;                      // this group's heads
+    float4 acc[J::HPG];
+#pragma unroll
+    for (int i = 0; i < J::HPG; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (grp < J::HS * J::PS) {
+#pragma unroll(8 / J::HPG)
+      for (int c = grp / J::HS; c < n; c += J::PS) {
+        const float4* part = reinterpret_cast<const float4*>(c ? rest + c * step : first) + (hb + hg) * (D / 4) + d4;
+#pragma unroll
+        for (int i = 0; i < J::HPG; ++i)
+          if (hb + hg + i < hd.nh) {
+            const float wv = js.w[c * J::H + hg + i];
+            const float4 x = __ldcg(part + i * (D / 4));
+            acc[i].x = fmaf(wv, x.x, acc[i].x);
+            acc[i].y = fmaf(wv, x.y, acc[i].y);
+            acc[i].z = fmaf(wv, x.z, acc[i].z);
+            acc[i].w = fmaf(wv, x.w, acc[i].w);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < J::HPG; ++i) {
+        const int at = (hg + i) * D + 4 * d4;
+        if constexpr (J::PS > 1) {
+          *reinterpret_cast<float4*>(&js.o[(grp / J::HS) * J::H * D + at]) = acc[i];
+        } else if (hb + hg + i < hd.nh) {
+          const size_t to = (bh0 + hb) * D + at;
+          paged_store(a, to, acc[i].x);
+          paged_store(a, to + 1, acc[i].y);
+          paged_store(a, to + 2, acc[i].z);
+          paged_store(a, to + 3, acc[i].w);
+        }
+      }
+    }
+    sync();
+    if constexpr (J::PS > 1) {
+      const int ne = min(J::H, hd.nh - hb) * D;
+      for (int e = tid; e < ne; e += kThreads) {
+        float x = 0.f;
+#pragma unroll
+        for (int p = 0; p < J::PS; ++p) x += js.o[p * J::H * D + e];
+        paged_store(a, (bh0 + hb) * D + e, x);
+      }
+      sync();     // js is free
+    }
   }
 }
 
