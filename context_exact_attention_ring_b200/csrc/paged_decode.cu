@@ -15,10 +15,15 @@
 // One CTA per SM; warp roles:
 //   warps 0-3  softmax: thread t owns tensor-memory lane t (key row t of S^T,
 //              dim t of O^T);
-//   warp 4     producer: lane i owns page slot i of a tile (a tile holds
-//              128 / page_size pages, or is part of one).  It looks the page
-//              up one tile ahead and issues the page's TMA boxes into a ring
-//              of 3 stages, next to the page's number of valid keys;
+//   warps 4, 6 producers of K (and Q) and of V: lane i owns page slot i of a
+//              tile (a tile holds 128 / page_size pages, or is part of one)
+//              and looks its page up one tile ahead; one lane then issues the
+//              pages' TMA boxes into a ring of 3 stages.  Issuing a box takes
+//              60-80 cycles, and a tile of 16-token pages is 32 boxes in the
+//              2700 cycles its bytes take: hence two warps.  The V producer
+//              also leaves each slot's number of valid keys (its stage is
+//              not refilled before the softmax is done with the tile, as K's
+//              is);
 //   warp 5     MMA issuer and tensor-memory owner.  Tiles follow each other
 //              across segments without a drain: S^T(t+1) is issued before
 //              O^T(t), and Q, O^T and the weights have two buffers.
@@ -46,7 +51,7 @@ constexpr int SLAB = kPagedTile * 128;      // 128 rows x 64 columns of bf16 (16
 constexpr int TILE_BYTES = 2 * SLAB;        // one K or V tile
 constexpr int QSLAB = NQ * 128;
 constexpr int CT = 128;                     // softmax threads
-constexpr int THREADS = CT + 64;
+constexpr int THREADS = CT + 96;
 constexpr uint32_t TMEM_COLS = 128;         // S^T 2 x 16, O^T 2 x (16 or 32)
 constexpr float LAZY = 8.f;                 // log2 of the growth tolerated before the base moves
 constexpr int MAX_SLOTS = kPagedTile / 8;   // page slots of a tile
@@ -62,12 +67,14 @@ struct PagedSmem {
   alignas(1024) uint8_t kv[pdt::NST][2][pdt::TILE_BYTES];
   alignas(1024) uint8_t q[2][2 * pdt::QSLAB];
   alignas(1024) uint8_t pt[2][2 * PSLAB];
-  int nvalid[pdt::NST][pdt::MAX_SLOTS];       // valid keys per page slot
-  float red[2][4][GP];                        // cross-warp maxima, by tile parity
-  float suml[2][4][GP], base[2][GP];          // cross-warp sums and final bases, by piece parity
+  int nvalid[pdt::NST][pdt::MAX_SLOTS];       // valid keys per page slot of a V stage
+  alignas(16) float red[2][GP][4];            // the warps' maxima, by tile parity
+  alignas(16) float suml[2][GP][4];           // the warps' sums, by piece parity
+  float base[2][GP];                          // final bases
   alignas(16) typename PagedJoin<pdt::CT, G, DH>::Smem join;
-  alignas(8) uint64_t kv_full[pdt::NST], kv_empty[pdt::NST];
-  alignas(8) uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], o_done[2], o_full[2], o_free[2], teardown;
+  // mbarriers
+  alignas(8) uint64_t k_full[pdt::NST], k_empty[pdt::NST], v_full[pdt::NST], v_empty[pdt::NST];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], s_free[2], o_done[2], o_full[2], o_free[2], teardown;
   PagedRunSmem run;
   uint32_t tmem_base;
   int is_last, abort_flag;
@@ -121,6 +128,17 @@ __device__ __forceinline__ void paged_tmem_st(uint32_t t, const float (&v)[N]) {
     tmem_st16(t, r);
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Maximum over the warp's lanes (NaN ignored, as fmaxf does).
 __device__ __forceinline__ float warp_max_redux(float v) {
   float r;
@@ -143,6 +161,13 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
   const PagedRows rows = paged_rows(a);
   const int psn_log2 = min(a.ps_log2, 7), psn = 1 << psn_log2;   // rows of a page slot
 
+  const int mine = paged_first_tiles(a);   // on its way during the setup
+  if (threadIdx.x == 4 * 32) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+  }
+  if (threadIdx.x == 6 * 32) tma_prefetch_desc(&tmV);
+
   // padded query rows and weight columns stay zero
   {
     uint4* z = reinterpret_cast<uint4*>(&sm.q[0][0]);
@@ -156,23 +181,16 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
       }
     fence_proxy_async_smem();
   }
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(smem_u32(&sm.kv_full[s]), 1);
-      mbar_init(smem_u32(&sm.kv_empty[s]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sm.q_full[i]), 1);
-      mbar_init(smem_u32(&sm.q_empty[i]), 1);
-      mbar_init(smem_u32(&sm.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.s_free[i]), CT);
-      mbar_init(smem_u32(&sm.p_full[i]), CT);
-      mbar_init(smem_u32(&sm.o_done[i]), 1);
-      mbar_init(smem_u32(&sm.o_full[i]), 1);
-      mbar_init(smem_u32(&sm.o_free[i]), CT);
-    }
-    mbar_init(smem_u32(&sm.teardown), 1);
-    sm.abort_flag = 0;
+  if (warp == 0) {
+    // a lane per barrier; those the softmax threads arrive on count all of them
+    constexpr int NB = 4 * NST + 17;
+    static_assert(NB <= 32, "a lane per barrier");
+    const uint32_t first = smem_u32(&sm.k_full[0]);
+    const uint32_t bar = first + 8 * lane;
+    const bool by_all = (bar >= smem_u32(&sm.p_full[0]) && bar < smem_u32(&sm.o_done[0])) ||
+                        (bar >= smem_u32(&sm.o_free[0]) && bar < smem_u32(&sm.teardown));
+    if (lane < NB) mbar_init(bar, by_all ? CT : 1);
+    if (lane == 0) sm.abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
@@ -181,76 +199,93 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const PagedRun run = paged_run<THREADS>(a, sm.run, SEG_COST, PARTS_PER_TILE);   // synchronises the CTA
+  const PagedRun run = paged_run<THREADS>(a, sm.run, mine, SEG_COST, PARTS_PER_TILE);   // synchronises the CTA
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  if (warp == 4) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-    }
+  if (warp == 4 || warp == 6) {
+    // ------------------------------------------------------------ producers
+    const bool is_k = warp == 4;
+    const CUtensorMap* tmKV = is_k ? &tmK : &tmV;
+    uint64_t* full = is_k ? sm.k_full : sm.v_full;
+    uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
     const uint64_t pol_kv = l2_policy_evict_first(), pol_q = l2_policy_evict_last();
     const int nslots = kPagedTile >> psn_log2;
     PagedWalk walk(run, SEG_COST);
     PagedPiece pc;
-    uint32_t cnt = 0, nq = 0;
-    bool ok = true;
-    while (ok && walk.next(a, rows, pc)) {
-      const PagedHead hd = paged_head(a, pc.row, pc.sub, NQ);
-      const int len = paged_len(a, hd.b);
-      const int qb = nq & 1;
-      if (nq >= 2) ok = mbar_wait(smem_u32(&sm.q_empty[qb]), ((nq >> 1) - 1) & 1u, abort_flag, kWaitQEmpty, err);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (lane == 0) {
-        const uint32_t qf = smem_u32(&sm.q_full[qb]);
-        mbar_arrive_expect_tx(qf, (uint32_t)maps.q_rows * DH * 2);
-        for (int sl = 0; sl < DH / 64; ++sl)
-          tma_load_4d(smem_u32(sm.q[qb]) + sl * QSLAB, &tmQ, qf, sl * 64, hd.h0, hd.b, 0, pol_q);
-      }
-      ++nq;
-      auto span = [&](int j) {
-        PagedSpan s;
-        s.valid = 0;
-        s.page = s.in_page = 0;
-        if (lane < nslots) s = paged_span(a, hd.b, hd.g, len, j * kPagedTile + (lane << psn_log2), psn);
-        return s;
-      };
-      PagedSpan next = span(pc.a);
-      for (int j = pc.a; j < pc.b; ++j) {
-        const PagedSpan cur = next;
-        if (j + 1 < pc.b) next = span(j + 1);
-        const int s = cnt % NST;
-        ok = mbar_wait(smem_u32(&sm.kv_empty[s]), ((cnt / NST) & 1u) ^ 1u, abort_flag, kWaitDecodeEmpty, err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const bool live = cur.valid > 0;
-        const uint32_t npages = __popc(__ballot_sync(0xffffffffu, live));
-        if (lane < MAX_SLOTS) sm.nvalid[s][lane] = cur.valid;
-        __syncwarp();
-        const uint32_t fb = smem_u32(&sm.kv_full[s]);
-        if (lane == 0) mbar_arrive_expect_tx(fb, npages * (uint32_t)(2 * DH * 2) << psn_log2);
-        __syncwarp();
-        if (live) {
-          const int c1 = maps.head_outer ? cur.in_page : hd.g, c2 = maps.head_outer ? hd.g : cur.in_page;
-          const uint32_t dst = (uint32_t)lane << (psn_log2 + 7);
-#pragma unroll
-          for (int sl = 0; sl < DH / 64; ++sl) {
-            tma_load_4d(smem_u32(sm.kv[s][0]) + sl * SLAB + dst, &tmK, fb, sl * 64, c1, c2, cur.page, pol_kv);
-            tma_load_4d(smem_u32(sm.kv[s][1]) + sl * SLAB + dst, &tmV, fb, sl * 64, c1, c2, cur.page, pol_kv);
-          }
-        }
-        ++cnt;
-      }
+    PagedHead hd{};
+    int len = 0;
+    auto span = [&](int j) {
+      PagedSpan s;
+      s.valid = 0;
+      s.page = s.in_page = 0;
+      if (lane < nslots) s = paged_span(a, hd.b, hd.g, len, j * kPagedTile + (lane << psn_log2), psn);
+      return s;
+    };
+    // the tile after the one being loaded: its piece, and its pages (looked up one tile ahead)
+    int j = 0;
+    bool more = walk.next(a, rows, pc), starts = true;
+    PagedSpan next;
+    if (more) {
+      hd = paged_head(a, pc.row, pc.sub, NQ);
+      len = paged_len(a, hd.b);
+      j = pc.a;
+      next = span(j);
     }
+    uint32_t cnt = 0, nq = 0;
+    while (more) {
+      const PagedSpan cur = next;
+      const int g = hd.g, h0 = hd.h0, b = hd.b;
+      const bool new_q = starts;
+      starts = ++j == pc.b;
+      if (starts) {
+        more = walk.next(a, rows, pc);
+        if (more) {
+          hd = paged_head(a, pc.row, pc.sub, NQ);
+          len = paged_len(a, hd.b);
+          j = pc.a;
+        }
+      }
+      if (more) next = span(j);
+      if (new_q && is_k) {
+        const int qb = nq & 1;
+        bool ok = nq < 2 || mbar_wait(smem_u32(&sm.q_empty[qb]), ((nq >> 1) - 1) & 1u, abort_flag, kWaitQEmpty, err);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (elect_one()) {
+          const uint32_t qf = smem_u32(&sm.q_full[qb]);
+          mbar_arrive_expect_tx(qf, (uint32_t)maps.q_rows * DH * 2);
+          for (int sl = 0; sl < DH / 64; ++sl)
+            tma_load_4d(smem_u32(sm.q[qb]) + sl * QSLAB, &tmQ, qf, sl * 64, h0, b, 0, pol_q);
+        }
+        ++nq;
+      }
+      const int s = cnt % NST;
+      const bool ok = mbar_wait(smem_u32(&empty[s]), ((cnt / NST) & 1u) ^ 1u, abort_flag, kWaitDecodeEmpty, err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint32_t live = __ballot_sync(0xffffffffu, cur.valid > 0);
+      if (!is_k && lane < MAX_SLOTS) sm.nvalid[s][lane] = cur.valid;
+      __syncwarp();
+      const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(sm.kv[s][is_k ? 0 : 1]);
+      if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(live) * (uint32_t)(DH * 2) << psn_log2);
+      __syncwarp();
+      for (uint32_t rest = live; rest; rest &= rest - 1) {
+        const int slot = __ffs(rest) - 1;
+        const int page = __shfl_sync(0xffffffffu, cur.page, slot), in_page = __shfl_sync(0xffffffffu, cur.in_page, slot);
+        const int c1 = maps.head_outer ? in_page : g, c2 = maps.head_outer ? g : in_page;
+        const uint32_t at = dst + ((uint32_t)slot << (psn_log2 + 7));
+        if (elect_one()) {
+#pragma unroll
+          for (int sl = 0; sl < DH / 64; ++sl) tma_load_4d(at + sl * SLAB, tmKV, fb, sl * 64, c1, c2, page, pol_kv);
+        }
+      }
+      ++cnt;
+    }
+    __syncwarp();
     // do not leave while copies are still landing in shared memory
     if (lane == 0) {
       for (uint32_t c = (cnt > (uint32_t)NST ? cnt - NST : 0); c < cnt; ++c)
-        mbar_wait(smem_u32(&sm.kv_full[c % NST]), (c / NST) & 1u, nullptr, kWaitTeardown, err);
+        mbar_wait(smem_u32(&full[c % NST]), (c / NST) & 1u, nullptr, kWaitTeardown, err);
       for (uint32_t c = (nq > 2u ? nq - 2u : 0u); c < nq; ++c)
         mbar_wait(smem_u32(&sm.q_full[c & 1]), (c >> 1) & 1u, nullptr, kWaitTeardown, err);
     }
@@ -267,7 +302,9 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
       // O^T += V^T P^T of tile tt
       auto pv = [&](uint32_t tt) -> bool {
         const uint32_t s = tt % NST, pb = tt & 1u, ob = prev_u & 1u;
-        if (!mbar_wait(smem_u32(&sm.p_full[pb]), (tt >> 1) & 1u, abort_flag, kWaitPFull, err)) return false;
+        if (!mbar_wait(smem_u32(&sm.v_full[s]), (tt / NST) & 1u, abort_flag, kWaitDecodeFull, err) ||
+            !mbar_wait(smem_u32(&sm.p_full[pb]), (tt >> 1) & 1u, abort_flag, kWaitPFull, err))
+          return false;
         if (prev_first && prev_u >= 2 &&
             !mbar_wait(smem_u32(&sm.o_free[ob]), ((prev_u >> 1) - 1) & 1u, abort_flag, kWaitOFinal, err))
           return false;
@@ -280,7 +317,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
           mma_ss(tO, vdesc + ((k * 16 * 128) >> 4), pdesc + ((((k >> 2) * PSLAB) + (k & 3) * 32) >> 4), idPV,
                  (!prev_first || k > 0) ? 1u : 0u);
         mma_commit(smem_u32(&sm.o_done[pb]));
-        mma_commit(smem_u32(&sm.kv_empty[s]));
+        mma_commit(smem_u32(&sm.v_empty[s]));
         if (prev_last) mma_commit(smem_u32(&sm.o_full[ob]));
         return true;
       };
@@ -290,7 +327,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
         const uint64_t qdesc = sw128_desc(smem_u32(sm.q[qb]), 16, 1024);
         for (int j = pc.a; j < pc.b && ok; ++j) {
           const uint32_t s = t % NST, sb = t & 1u;
-          if (!mbar_wait(smem_u32(&sm.kv_full[s]), (t / NST) & 1u, abort_flag, kWaitDecodeFull, err) ||
+          if (!mbar_wait(smem_u32(&sm.k_full[s]), (t / NST) & 1u, abort_flag, kWaitDecodeFull, err) ||
               (t >= 2 && !mbar_wait(smem_u32(&sm.s_free[sb]), ((t >> 1) - 1) & 1u, abort_flag, kWaitSFull, err))) {
             ok = false;
             break;
@@ -302,6 +339,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
             mma_ss(tmem + 16 * sb, kdesc + ((((k >> 2) * SLAB) + (k & 3) * 32) >> 4),
                    qdesc + ((((k >> 2) * QSLAB) + (k & 3) * 32) >> 4), idS, k > 0 ? 1u : 0u);
           mma_commit(smem_u32(&sm.s_full[sb]));
+          mma_commit(smem_u32(&sm.k_empty[s]));
           if (j == pc.b - 1) mma_commit(smem_u32(&sm.q_empty[qb]));
           if (t > 0) ok = pv(t - 1);
           prev_first = j == pc.a;
@@ -349,29 +387,35 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
         float s = fl[h];
 #pragma unroll
         for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        if (lane == 0) sm.suml[ob][warp][h] = s;
+        if (lane == 0) sm.suml[ob][h][warp] = s;
       }
       if (named_bar_any(1, CT, !fin)) return false;
       const bool whole = fpc.a == 0 && fpc.b == fpc.nt;
       float* part = paged_part(a, blockIdx.x, run.t0 >= fpc.seg_t ? 0 : 1);
+      const size_t bh0 = (size_t)fhd.b * a.Hq + fhd.h0;
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         if (h >= fhd.nh) continue;
-        const float L = (sm.suml[ob][0][h] + sm.suml[ob][1][h]) + (sm.suml[ob][2][h] + sm.suml[ob][3][h]);
-        const float od = L == 0.f ? 0.f : (o[h] + olo[h]) / L;
-        const float lse = L == 0.f ? -CUDART_INF_F : (sm.base[ob][h] + log2f(L)) * 0.6931471805599453f;
+        const float4 r = *reinterpret_cast<const float4*>(sm.suml[ob][h]);
+        const float L = (r.x + r.y) + (r.z + r.w);
+        const float od = L == 0.f ? 0.f : __fdividef(o[h] + olo[h], L);
         if (row >= DH) continue;      // D = 64: the upper half of O^T is padding
-        if (whole) {
-          const size_t bh = (size_t)fhd.b * a.Hq + fhd.h0 + h;
-          paged_store(a, bh * DH + row, od);
-          if (row == 0 && a.out_lse) a.out_lse[bh] = lse;
-        } else {
+        if (whole)
+          paged_store(a, (bh0 + h) * DH + row, od);
+        else
           part[h * DH + row] = od;
-          if (row == 0) part[kPagedHeads * DH + h] = lse;
-        }
+      }
+      if (row < fhd.nh) {
+        const float4 r = *reinterpret_cast<const float4*>(sm.suml[ob][row]);
+        const float L = (r.x + r.y) + (r.z + r.w);
+        const float lse = L == 0.f ? -CUDART_INF_F : (sm.base[ob][row] + log2f(L)) * 0.6931471805599453f;
+        if (!whole)
+          part[kPagedHeads * DH + row] = lse;
+        else if (a.out_lse)
+          a.out_lse[bh0 + row] = lse;
       }
       if (!whole) {
-        const int c0 = run_owner(run.T, run.n, fpc.seg_t), c1 = run_owner(run.T, run.n, fpc.seg_t + fpc.nt - 1);
+        const int c0 = run_owner(run, fpc.seg_t), c1 = run_owner(run, fpc.seg_t + fpc.nt - 1);
         named_bar_sync(1, CT);      // the part is written
         if (row == 0) {
           const unsigned int old = atom_add_acq_rel_gpu(a.ws_count + c0, 1u);
@@ -398,8 +442,8 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
       }
       for (int j = pc.a; j < pc.b; ++j, ++t) {
         const uint32_t sb = t & 1u, st = t % NST;
-        // the stage's valid counts, the scores, and a weight buffer that O^T has taken
-        bool good = mbar_wait(smem_u32(&sm.kv_full[st]), (t / NST) & 1u, abort_flag, kWaitDecodeFull, err);
+        // the tile's valid counts, the scores, and a weight buffer that O^T has taken
+        bool good = mbar_wait(smem_u32(&sm.v_full[st]), (t / NST) & 1u, abort_flag, kWaitDecodeFull, err);
         if (good) good = mbar_wait(smem_u32(&sm.s_full[sb]), (t >> 1) & 1u, abort_flag, kWaitSFull, err);
         if (good && t >= 2)
           good = mbar_wait(smem_u32(&sm.o_done[sb]), ((t >> 1) - 1) & 1u, abort_flag, kWaitPFull, err);
@@ -412,12 +456,14 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
         mbar_arrive(smem_u32(&sm.s_free[sb]));
         const bool valid = in_slot < sm.nvalid[st][slot];
         if (!valid) {
+          // neighbouring rows start at different 16-byte columns: 4 rows a wavefront, not 1
           uint4* vr = reinterpret_cast<uint4*>(sm.kv[st][1] + row * 128);
 #pragma unroll
           for (int sl = 0; sl < DH / 64; ++sl)
 #pragma unroll
-            for (int c = 0; c < 8; ++c) vr[sl * (SLAB / 16) + c] = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < 8; ++c) vr[sl * (SLAB / 16) + ((c + row) & 7)] = make_uint4(0u, 0u, 0u, 0u);
         }
+        __syncwarp();
         bool exceed = false;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
@@ -430,7 +476,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
 #pragma unroll
           for (int h = 0; h < G; ++h) {
             const float mw = warp_max_redux(xs[h]);
-            if (lane == 0) sm.red[rb][warp][h] = mw;
+            if (lane == 0) sm.red[rb][h][warp] = mw;
           }
           if (named_bar_any(1, CT, !good)) {
             ok = false;
@@ -440,7 +486,8 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
           bool moved = false;
 #pragma unroll
           for (int h = 0; h < G; ++h) {
-            const float mt = fmaxf(fmaxf(sm.red[rb][0][h], sm.red[rb][1][h]), fmaxf(sm.red[rb][2][h], sm.red[rb][3][h]));
+            const float4 r = *reinterpret_cast<const float4*>(sm.red[rb][h]);
+            const float mt = fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w));
             alpha[h] = 1.f;
             if (mt > m[h] + LAZY) {
               alpha[h] = m[h] == -CUDART_INF_F ? 0.f : ex2(m[h] - mt);

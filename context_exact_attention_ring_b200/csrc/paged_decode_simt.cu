@@ -60,7 +60,8 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
   __shared__ SimtSmem<G, D> sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = lane >> 4, l16 = lane & 15;
   const PagedRows rows = paged_rows(a);
-  const PagedRun run = paged_run<THREADS>(a, sm.run, SEG_COST, PARTS_PER_TILE);
+  const int mine = paged_first_tiles(a);
+  const PagedRun run = paged_run<THREADS>(a, sm.run, mine, SEG_COST, PARTS_PER_TILE);
   paged_empty_rows(a, tid, THREADS);
   const float sl2 = a.scale * 1.4426950408889634f;
   PagedWalk walk(run, SEG_COST);
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
     }
     __syncthreads();    // the parts are written, sm.o is free
     if (!whole) {
-      const int c0 = run_owner(run.T, run.n, pc.seg_t), c1 = run_owner(run.T, run.n, pc.seg_t + pc.nt - 1);
+      const int c0 = run_owner(run, pc.seg_t), c1 = run_owner(run, pc.seg_t + pc.nt - 1);
       if (tid == 0) {
         const unsigned int old = atom_add_acq_rel_gpu(a.ws_count + c0, 1u);
         sm.last = old == (unsigned int)(c1 - c0);

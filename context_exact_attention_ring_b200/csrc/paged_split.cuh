@@ -2,8 +2,8 @@
 //
 // The keys of every (sequence, kv head, head group) -- a segment -- are cut
 // into tiles of 128, and all tiles of the call, segment after segment, are
-// dealt to n CTAs in n equal contiguous runs (CTA c gets units
-// [cT/n, (c+1)T/n) of T, where a unit is a tile or a segment's fixed cost).  Ragged batches balance whatever their lengths, one
+// dealt to n CTAs in n contiguous runs of as many units (a unit is a tile or a
+// segment's fixed cost), give or take one.  Ragged batches balance whatever their lengths, one
 // long sequence spreads over the whole GPU, and the lengths are read on the
 // device, so a captured launch follows them.  A run covers whole segments,
 // whose result is written at once, and at most two parts of segments (at its
@@ -49,15 +49,19 @@ __device__ __forceinline__ int paged_units(int tiles, int seg_cost) { return til
 struct PagedRun {
   int T;          // units of the call
   int n;          // CTAs that have work
+  int q, r;       // T = n q + r: the first r CTAs get q + 1 units, the others q
   int t0, t1;     // this CTA's units
   int row;        // row that holds t0
   int row_t;      // first unit of that row
 };
-__device__ __forceinline__ int run_start(int T, int n, int c) { return (int)((long long)c * T / n); }
-__device__ __forceinline__ int run_owner(int T, int n, int t) { return (int)(((long long)(t + 1) * n - 1) / T); }
+__device__ __forceinline__ int run_start(const PagedRun& r, int c) { return c * r.q + min(c, r.r); }
+__device__ __forceinline__ int run_owner(const PagedRun& r, int t) {
+  const int big = r.r * (r.q + 1);
+  return t < big ? t / (r.q + 1) : r.r + (t - big) / r.q;
+}
 
 struct PagedRunSmem {
-  int warp_sum[32], warp_rows[32];
+  int units[32], rows[32], more[32];    // per warp
   int row, row_t;
 };
 
@@ -65,74 +69,91 @@ struct PagedRunSmem {
 // parts_per_tile: how many parts a segment may be cut into for every tile of
 // a part.  Joining takes as long as a tile for every parts_per_tile parts, so
 // that cutting n parts of T / n tiles is longest at n^2 = parts_per_tile T.
+// mine: the tiles of row threadIdx.x (paged_first_tiles), loaded earlier.
+__device__ __forceinline__ int paged_first_tiles(const PagedDecodeArgs& a) {
+  return (int)threadIdx.x < paged_rows(a).R ? paged_tiles(a, threadIdx.x) : 0;
+}
 template <int kThreads>
-__device__ __forceinline__ PagedRun paged_run(const PagedDecodeArgs& a, PagedRunSmem& s, int seg_cost,
+__device__ __forceinline__ PagedRun paged_run(const PagedDecodeArgs& a, PagedRunSmem& s, int mine, int seg_cost,
                                               int parts_per_tile) {
   constexpr int NW = kThreads / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const PagedRows rows = paged_rows(a);
-  // all tiles and all rows with keys; the first kThreads rows stay in registers
-  const int mine = tid < rows.R ? paged_tiles(a, tid) : 0;
-  int sum = mine, some = mine > 0;
+  auto scan = [&](int x) {    // inclusive, over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += up;
+    }
+    return x;
+  };
+  // the first kThreads rows' units up to each row, and the sums over all rows
+  const int units0 = paged_units(mine, seg_cost), incl0 = scan(units0);
+  int some = __popc(__ballot_sync(0xffffffffu, mine > 0)), more_tiles = 0, more_rows = 0;
   for (int r = tid + kThreads; r < rows.R; r += kThreads) {
     const int nt = paged_tiles(a, r);
-    sum += nt;
-    some += nt > 0;
+    more_tiles += nt;
+    more_rows += nt > 0;
   }
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  some = __reduce_add_sync(0xffffffffu, some);
-  if (lane == 0) {
-    s.warp_sum[warp] = sum;
-    s.warp_rows[warp] = some;
+  if (rows.R > kThreads) {
+    more_tiles = __reduce_add_sync(0xffffffffu, more_tiles);
+    more_rows = __reduce_add_sync(0xffffffffu, more_rows);
+  }
+  if (lane == 31) {
+    s.units[warp] = incl0;
+    s.rows[warp] = some + more_rows;
+    s.more[warp] = more_tiles + more_rows * seg_cost;
   }
   __syncthreads();
-  int tiles = 0, segs = 0;
+  int units = 0, segs = 0, more = 0, before = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    tiles += s.warp_sum[w];
-    segs += s.warp_rows[w];
+    if (w == warp) before = units;
+    units += s.units[w];
+    segs += s.rows[w];
+    more += s.more[w];
   }
   PagedRun run;
-  run.T = (tiles + segs * seg_cost) * rows.mult;
-  tiles *= rows.mult;
+  run.T = (units + more) * rows.mult;
   segs *= rows.mult;
+  const int tiles = run.T - segs * seg_cost;
   run.n = max(1, min(min((int)gridDim.x, tiles), (int)sqrtf((float)parts_per_tile * tiles * segs)));
-  run.row = run.row_t = 0;
+  run.row = run.row_t = run.q = run.r = 0;
   const int c = blockIdx.x;
   if (run.T == 0 || c >= run.n) {
     run.t0 = run.t1 = 0;
     return run;
   }
-  run.t0 = run_start(run.T, run.n, c);
-  run.t1 = run_start(run.T, run.n, c + 1);
+  run.q = run.T / run.n;
+  run.r = run.T - run.n * run.q;
+  run.t0 = run_start(run, c);
+  run.t1 = run_start(run, c + 1);
   // the row that holds t0
   const int want = run.t0 / rows.mult;    // units counted once per row
-  int base = 0;
-  for (int r0 = 0; r0 < rows.R; r0 += kThreads) {
+  int hi = before + incl0, lo = hi - units0, base = units;
+  if (lo <= want && want < hi) {
+    s.row = tid;
+    s.row_t = lo * rows.mult;
+  }
+  for (int r0 = kThreads; r0 < rows.R && want >= base; r0 += kThreads) {    // the same in every thread
     const int r = r0 + tid;
-    const int nu = paged_units(r0 == 0 ? mine : (r < rows.R ? paged_tiles(a, r) : 0), seg_cost);
-    int incl = nu;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
-    }
-    __syncthreads();    // warp_sum is free
-    if (lane == 31) s.warp_sum[warp] = incl;
+    const int nu = paged_units(r < rows.R ? paged_tiles(a, r) : 0, seg_cost), incl = scan(nu);
+    __syncthreads();    // s.units is free
+    if (lane == 31) s.units[warp] = incl;
     __syncthreads();
-    int before = base, chunk = 0;
+    hi = base + incl;
+    int chunk = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      if (w < warp) before += s.warp_sum[w];
-      chunk += s.warp_sum[w];
+      if (w < warp) hi += s.units[w];
+      chunk += s.units[w];
     }
-    const int hi = before + incl, lo = hi - nu;
+    lo = hi - nu;
     if (lo <= want && want < hi) {
       s.row = r;
       s.row_t = lo * rows.mult;
     }
     base += chunk;
-    if (want < base) break;    // the same in every thread
   }
   __syncthreads();
   run.row = s.row;
@@ -250,23 +271,25 @@ __device__ __forceinline__ float* paged_part(const PagedDecodeArgs& a, int c, in
   return a.ws_part + (size_t)(c * 2 + slot) * kPagedHeads * (a.D + 1);
 }
 
-// Joins the parts of a segment (of its CTAs c0..c1) and writes the result, 8
+// Joins the parts of a segment (of its CTAs c0..c1) and writes the result, 4
 // heads at a time.  Called by kThreads threads after the acquire of the last
-// arrival; sync() is their barrier.  First a warp takes a head's lse values, a
-// lane every 32nd, all loaded at once, and leaves the weights in shared
-// memory.  Then D / 4 lanes to a row add the parts up, 4 dims each: the groups
-// of lanes share out the heads first and then the parts, and their 16-byte
-// loads wait for nothing but the weights.  (One thread per output looking the
-// parts up one after the other took 60 us of a 65 us call.)
+// arrival; sync() is their barrier.  A row of D dims takes D / 4 lanes; the
+// groups of lanes share out the parts, and a lane has 4 parts of 4 heads in
+// flight before it needs the first weight.  The weights come from the lse
+// values meanwhile: a warp to a head, a lane to every 32nd part.  The groups'
+// sums meet in shared memory.  (Of 9 to 16 heads, 8 at a time, the groups share
+// out the heads instead, which needs no shared memory for the sums.)  (One thread per output looking the parts up one
+// after the other took 60 us of a 65 us call.)
 template <int kThreads, int G, int D>
 struct PagedJoin {
-  static constexpr int H = G < 8 ? G : 8;                       // heads at a time
   static constexpr int NG = kThreads / (D / 4);                 // groups of lanes
-  static constexpr int HS = H < NG ? H : NG, PS = NG / HS;      // groups over heads, over parts
-  static constexpr int HPG = H / HS;                            // heads of a group
+  static constexpr bool BY_HEAD = G > 8;                        // groups over heads, not parts
+  static constexpr int H = BY_HEAD ? 8 : G < 4 ? G : 4;         // heads at a time
+  static constexpr int HL = BY_HEAD ? (H + NG - 1) / NG : H;    // heads of a lane
+  static constexpr int U = BY_HEAD ? 8 : 4;                     // parts a lane has in flight
   struct Smem {
     float w[kPagedMaxCtas * H];
-    alignas(16) float o[PS > 1 ? PS * H * D : 4];               // sums of the groups over parts
+    alignas(16) float4 o[BY_HEAD ? 1 : NG][BY_HEAD ? 1 : H][BY_HEAD ? 1 : D / 4];
   };
 };
 template <int kThreads, int G, int D, typename Sync>
@@ -274,18 +297,32 @@ __device__ __forceinline__ void paged_join(const PagedDecodeArgs& a, const Paged
                                            const PagedHead& hd, int c0, int c1, int tid,
                                            typename PagedJoin<kThreads, G, D>::Smem& js, Sync sync) {
   using J = PagedJoin<kThreads, G, D>;
-  constexpr int NW = kThreads / 32;
+  constexpr int NW = kThreads / 32, H = J::H, HL = J::HL, U = J::U;
+  constexpr int CS = J::BY_HEAD ? 1 : J::NG;                    // a lane's parts: cf, cf + CS, ...
   constexpr int KV = (kPagedMaxCtas + 31) / 32;                 // lse values per lane
   const int warp = tid >> 5, lane = tid & 31;
   const int n = c1 - c0 + 1;
-  const int slot0 = run_start(run.T, run.n, c0) >= pc.seg_t ? 0 : 1;
+  const int slot0 = run_start(run, c0) >= pc.seg_t ? 0 : 1;
   const int step = 2 * kPagedHeads * (D + 1);
   const float* first = paged_part(a, c0, slot0);
   const float* rest = paged_part(a, c0, 0);                     // part i > 0 at rest + i step
   const size_t bh0 = (size_t)hd.b * a.Hq + hd.h0;
   const int d4 = tid % (D / 4), grp = tid / (D / 4);
-  for (int hb = 0; hb < hd.nh; hb += J::H) {
-    for (int h = warp; h < J::H && hb + h < hd.nh; h += NW) {
+  const int cf = J::BY_HEAD ? 0 : grp, hl = J::BY_HEAD ? grp * HL : 0;
+  for (int hb = 0; hb < hd.nh; hb += H) {
+    const int mine = min(HL, min(H, hd.nh - hb) - hl);          // this lane's heads, from hb + hl on
+    float4 x[U][HL], acc[HL];
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int u = 0; u < U; ++u, c += CS) {
+        const float4* part = reinterpret_cast<const float4*>(c ? rest + c * step : first) + (hb + hl) * (D / 4) + d4;
+#pragma unroll
+        for (int h = 0; h < HL; ++h)
+          x[u][h] = c < n && h < mine ? __ldcg(part + h * (D / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    fetch(cf);
+    for (int h = warp; h < H && hb + h < hd.nh; h += NW) {
       float w[KV], mx = -CUDART_INF_F;
 #pragma unroll
       for (int k = 0; k < KV; ++k) {
@@ -307,54 +344,49 @@ __device__ __forceinline__ void paged_join(const PagedDecodeArgs& a, const Paged
       const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
       for (int k = 0; k < KV; ++k)
-        if (lane + 32 * k < n) js.w[(lane + 32 * k) * J::H + h] = w[k] * inv;
+        if (lane + 32 * k < n) js.w[(lane + 32 * k) * H + h] = w[k] * inv;
       if (lane == 0 && a.out_lse) a.out_lse[bh0 + hb + h] = L == 0.f ? -CUDART_INF_F : mx + logf(L);
     }
+#pragma unroll
+    for (int h = 0; h < HL; ++h) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
     sync();
-    const int hg = (grp % J::HS) * J::HPG;                      // this group's heads
-    float4 acc[J::HPG];
+    for (int c = cf; c < n; c += U * CS) {
 #pragma unroll
-    for (int i = 0; i < J::HPG; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (grp < J::HS * J::PS) {
-#pragma unroll(8 / J::HPG)
-      for (int c = grp / J::HS; c < n; c += J::PS) {
-        const float4* part = reinterpret_cast<const float4*>(c ? rest + c * step : first) + (hb + hg) * (D / 4) + d4;
+      for (int u = 0; u < U; ++u)
+        if (c + u * CS < n)
 #pragma unroll
-        for (int i = 0; i < J::HPG; ++i)
-          if (hb + hg + i < hd.nh) {
-            const float wv = js.w[c * J::H + hg + i];
-            const float4 x = __ldcg(part + i * (D / 4));
-            acc[i].x = fmaf(wv, x.x, acc[i].x);
-            acc[i].y = fmaf(wv, x.y, acc[i].y);
-            acc[i].z = fmaf(wv, x.z, acc[i].z);
-            acc[i].w = fmaf(wv, x.w, acc[i].w);
+          for (int h = 0; h < HL; ++h) {
+            const float wv = h < mine ? js.w[(c + u * CS) * H + hl + h] : 0.f;
+            acc[h].x = fmaf(wv, x[u][h].x, acc[h].x);
+            acc[h].y = fmaf(wv, x[u][h].y, acc[h].y);
+            acc[h].z = fmaf(wv, x[u][h].z, acc[h].z);
+            acc[h].w = fmaf(wv, x[u][h].w, acc[h].w);
           }
-      }
+      if (c + U * CS < n) fetch(c + U * CS);
+    }
+    if constexpr (J::BY_HEAD) {
 #pragma unroll
-      for (int i = 0; i < J::HPG; ++i) {
-        const int at = (hg + i) * D + 4 * d4;
-        if constexpr (J::PS > 1) {
-          *reinterpret_cast<float4*>(&js.o[(grp / J::HS) * J::H * D + at]) = acc[i];
-        } else if (hb + hg + i < hd.nh) {
-          const size_t to = (bh0 + hb) * D + at;
-          paged_store(a, to, acc[i].x);
-          paged_store(a, to + 1, acc[i].y);
-          paged_store(a, to + 2, acc[i].z);
-          paged_store(a, to + 3, acc[i].w);
+      for (int h = 0; h < HL; ++h)
+        if (h < mine) {
+          const size_t to = (bh0 + hb + hl + h) * D + 4 * d4;
+          paged_store(a, to, acc[h].x);
+          paged_store(a, to + 1, acc[h].y);
+          paged_store(a, to + 2, acc[h].z);
+          paged_store(a, to + 3, acc[h].w);
         }
-      }
-    }
-    sync();
-    if constexpr (J::PS > 1) {
-      const int ne = min(J::H, hd.nh - hb) * D;
-      for (int e = tid; e < ne; e += kThreads) {
-        float x = 0.f;
+    } else {
 #pragma unroll
-        for (int p = 0; p < J::PS; ++p) x += js.o[p * J::H * D + e];
-        paged_store(a, (bh0 + hb) * D + e, x);
+      for (int h = 0; h < H; ++h) js.o[grp][h][d4] = acc[h];
+      sync();
+      const int ne = min(H, hd.nh - hb) * D;
+      for (int e = tid; e < ne; e += kThreads) {
+        float o = 0.f;
+#pragma unroll
+        for (int p = 0; p < J::NG; ++p) o += reinterpret_cast<const float*>(js.o[p])[e];
+        paged_store(a, (bh0 + hb) * D + e, o);
       }
-      sync();     // js is free
     }
+    sync();     // js is free
   }
 }
 
