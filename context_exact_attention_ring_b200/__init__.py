@@ -478,64 +478,75 @@ def ring_attn_kv_append(k_cache, v_cache, k_new, v_new, shard_lens, n_appended, 
 # paged KV cache (layouts and rules: include/ring_attn.h)
 # ---------------------------------------------------------------------------
 def _one_device(*ts):
-    """The CUDA device all given tensors live on."""
-    dev = None
+    """The index of the CUDA device all given tensors live on."""
+    dev = -2
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("tensors must live on a CUDA device")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("tensors must live on one device")
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError("tensors must live on a CUDA device")
+            if dev >= 0:
+                raise ValueError("tensors must live on one device")
+            dev = d
     return dev
+
+
+# current stream of a device as a plain integer (without making a Stream object, which costs 3 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _launch(name, dev, *args):
     """Call the library on the tensors' device, on that device's current torch stream."""
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    fn = getattr(_lib or lib(), name)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream().cuda_stream)
-    _check(st, name)
+            st = fn(*args, _raw_stream(dev))
+    if st != RING_OK:
+        _check(st, name)
 
 
 def _int32(what, t, shape):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
     return t.data_ptr()
 
 
-def _table(block_table, B=None):
+def _table(block_table, B):
     """(pointer, W, row stride) of a block table [B, W] (rows may be slices of wider ones)."""
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1 and block_table.shape[1] > 1 \
-            or (B is not None and block_table.shape[0] != B):
-        raise ValueError("block_table must be int32 [B, W] with contiguous rows")
-    n, W = block_table.shape
-    return block_table.data_ptr(), W, block_table.stride(0) if n > 1 else max(W, 1)
+    if block_table.dim() == 2 and block_table.dtype == torch.int32:
+        n, W = block_table.shape
+        sn, s1 = block_table.stride()
+        if n == B and (s1 == 1 or W == 1):
+            return block_table.data_ptr(), W, sn if n > 1 else max(W, 1)
+    raise ValueError("block_table must be int32 [B, W] with contiguous rows")
 
 
 def _pool(k_pool, v_pool=None):
     """(num_pages, page_size, Hkv, D, page, token and head strides) of cache pools [num_pages, page_size, Hkv, D]."""
-    if k_pool.dim() != 4 or k_pool.stride(3) != 1:
+    strides = k_pool.stride()
+    if len(strides) != 4 or strides[3] != 1:
         raise ValueError("pools must be [num_pages, page_size, Hkv, D] with contiguous last dimension")
-    if v_pool is not None and (v_pool.shape != k_pool.shape or v_pool.stride() != k_pool.stride() or
+    if v_pool is not None and (v_pool.shape != k_pool.shape or v_pool.stride() != strides or
                                v_pool.dtype != k_pool.dtype):
         raise ValueError("k_pool and v_pool must have one shape, dtype and strides")
     N, ps, Hkv, D = k_pool.shape
-    sp, st, sh, _ = k_pool.stride()
+    sp, st, sh, _ = strides
     # the stride of a dimension of length 1 says nothing
     return N, ps, Hkv, D, (sp if N > 1 else ps * st), (st if ps > 1 else Hkv * D), (sh if Hkv > 1 else D)
 
 
 def _rows3(what, x, shape, dtype):
     """(row stride, head stride) of x [n, heads, D] with contiguous D."""
-    if tuple(x.shape) != shape or x.dtype != dtype or x.stride(2) != 1:
-        raise ValueError(f"{what} must be {list(shape)} of the cache's dtype with contiguous last dimension")
-    return (x.stride(0) if shape[0] > 1 else shape[1] * shape[2]), (x.stride(1) if shape[1] > 1 else shape[2])
+    if x.shape == shape and x.dtype == dtype:
+        sn, sh, s1 = x.stride()
+        if s1 == 1:
+            return (sn if shape[0] > 1 else shape[1] * shape[2]), (sh if shape[1] > 1 else shape[2])
+    raise ValueError(f"{what} must be {list(shape)} of the cache's dtype with contiguous last dimension")
 
 
 def ring_attn_page_extend(seq_lens, new_lens, block_table, free_pages, n_free, page_size, max_tokens=None,
@@ -552,13 +563,13 @@ def ring_attn_page_extend(seq_lens, new_lens, block_table, free_pages, n_free, p
     if slot_map is None:
         if max_tokens is None:
             raise ValueError("give max_tokens or slot_map")
-        slot_map = torch.empty((int(max_tokens),), device=dev, dtype=torch.int32)
+        slot_map = seq_lens.new_empty((int(max_tokens),), dtype=torch.int32)
     elif max_tokens is not None and slot_map.numel() != int(max_tokens):
         raise ValueError("slot_map must have max_tokens entries")
     if start_lens is None:
-        start_lens = torch.empty((B,), device=dev, dtype=torch.int32)
+        start_lens = seq_lens.new_empty((B,), dtype=torch.int32)
     if cu_new is None:
-        cu_new = torch.empty((B + 1,), device=dev, dtype=torch.int32)
+        cu_new = seq_lens.new_empty((B + 1,), dtype=torch.int32)
     n, T = free_pages.numel(), slot_map.numel()
     _launch("ring_attn_page_extend", dev, _int32("seq_lens", seq_lens, (B,)), _int32("new_lens", new_lens, (B,)), tp,
             _int32("free_pages", free_pages, (n,)), _int32("n_free", n_free, (1,)),
@@ -623,15 +634,15 @@ def ring_attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, sel=None, n
         selp, nselp = _int32("sel", sel, (B, Hkv, K)), _int32("n_sel", n_sel, (B, Hkv))
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     if out is None:
-        out = torch.empty((B, Hq, D), device=dev, dtype=out_dtype or q.dtype)
+        out = q.new_empty((B, Hq, D), dtype=out_dtype or q.dtype)
     elif tuple(out.shape) != (B, Hq, D) or not out.is_contiguous() or (out_dtype or out.dtype) != out.dtype:
         raise ValueError("out must be contiguous [B, Hq, D] of out_dtype")
     if out_lse is None:
-        out_lse = torch.empty((B, Hq), device=dev, dtype=torch.float32)
+        out_lse = q.new_empty((B, Hq), dtype=torch.float32)
     elif tuple(out_lse.shape) != (B, Hq) or out_lse.dtype != torch.float32 or not out_lse.is_contiguous():
         raise ValueError("out_lse must be contiguous float32 [B, Hq]")
     if workspace is None:
-        workspace = decode_paged_workspace(D, dev)
+        workspace = decode_paged_workspace(D, q.device)
     elif not workspace.is_contiguous():
         raise ValueError("tensors must be contiguous")
     _launch("ring_attn_decode_paged", dev, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), tp,
@@ -650,7 +661,7 @@ def ring_attn_page_bounds(k_pool, block_table, seq_lens, bounds=None, start_lens
     B = seq_lens.numel()
     tp, W, ts = _table(block_table, B)
     if bounds is None:
-        bounds = torch.zeros((N, Hkv, 2, D), device=dev, dtype=k_pool.dtype)
+        bounds = k_pool.new_zeros((N, Hkv, 2, D))
     elif tuple(bounds.shape) != (N, Hkv, 2, D) or bounds.dtype != k_pool.dtype or not bounds.is_contiguous():
         raise ValueError("bounds must be contiguous [num_pages, Hkv, 2, D] of the cache's dtype")
     _launch("ring_attn_page_bounds", dev, k_pool.data_ptr(), bounds.data_ptr(), tp,
@@ -671,7 +682,7 @@ def ring_attn_page_scores(q, bounds, block_table, seq_lens, page_size, scores=No
     qb, qh = _rows3("q", q, (B, Hq, D), bounds.dtype)
     tp, W, ts = _table(block_table, B)
     if scores is None:
-        scores = torch.empty((B, Hkv, W), device=dev, dtype=torch.float32)
+        scores = q.new_empty((B, Hkv, W), dtype=torch.float32)
     elif tuple(scores.shape) != (B, Hkv, W) or scores.dtype != torch.float32 or not scores.is_contiguous():
         raise ValueError("scores must be contiguous float32 [B, Hkv, W]")
     _launch("ring_attn_page_scores", dev, q.data_ptr(), bounds.data_ptr(), tp, _int32("seq_lens", seq_lens, (B,)),
@@ -689,9 +700,9 @@ def ring_attn_page_select(scores, seq_lens, page_size, K, keep_first=1, keep_las
     B, Hkv, W = scores.shape
     K = int(K)
     if sel is None:
-        sel = torch.empty((B, Hkv, K), device=dev, dtype=torch.int32)
+        sel = seq_lens.new_empty((B, Hkv, K), dtype=torch.int32)
     if n_sel is None:
-        n_sel = torch.empty((B, Hkv), device=dev, dtype=torch.int32)
+        n_sel = seq_lens.new_empty((B, Hkv), dtype=torch.int32)
     _launch("ring_attn_page_select", dev, scores.data_ptr(), _int32("seq_lens", seq_lens, (B,)),
             _int32("sel", sel, (B, Hkv, K)), _int32("n_sel", n_sel, (B, Hkv)), B, Hkv, W, int(page_size), K,
             int(keep_first), int(keep_last))

@@ -13,6 +13,24 @@
 
 namespace ra {
 
+// Launches with programmatic stream serialization: the kernel may start while
+// the one before it on the stream finishes.  Every kernel launched so begins
+// with paged_begin(), before it touches global memory.
+template <typename... P, typename... A>
+inline cudaError_t paged_launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 struct PoolStrides {
   long long page, token, head;   // elements
 };

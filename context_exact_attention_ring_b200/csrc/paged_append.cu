@@ -9,7 +9,7 @@
 // is spread over as many threads as it has pieces and a prompt's over the GPU.
 #include <cuda_runtime.h>
 
-#include "paged.h"
+#include "paged.cuh"
 
 namespace ra {
 
@@ -21,6 +21,7 @@ constexpr int PER = 4;     // 16-byte pieces per thread
 __global__ void __launch_bounds__(pga::THREADS) paged_append_kernel(PagedAppendArgs a, int nvh, int nv) {
   using namespace pga;
   // nvh: pieces of a head's row, nv: of a token's K and V rows together (K first)
+  paged_begin();
   const long long total = (long long)a.T * nv;
   const long long first = (long long)blockIdx.x * (THREADS * PER);
   const int t0 = (int)(first / nv), e0 = (int)(first - (long long)t0 * nv);
@@ -57,8 +58,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st) {
   const long long total = (long long)a.T * nv, per = pga::THREADS * pga::PER;
   const long long blocks = (total + per - 1) / per;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  paged_append_kernel<<<(unsigned)blocks, pga::THREADS, 0, st>>>(a, nvh, nv);
-  return cudaGetLastError();
+  return paged_launch(paged_append_kernel, (unsigned)blocks, pga::THREADS, 0, st, a, nvh, nv);
 }
 
 }  // namespace ra

@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
   const PagedRows rows = paged_rows(a);
   const int psn_log2 = min(a.ps_log2, 7), psn = 1 << psn_log2;   // rows of a page slot
 
+  paged_begin();
   const int mine = paged_first_tiles(a);   // on its way during the setup
   if (threadIdx.x == 4 * 32) {
     tma_prefetch_desc(&tmQ);
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     }
     uint32_t cnt = 0, nq = 0;
     while (more) {
-      const PagedSpan cur = next;
+      PagedSpan cur = next;
       const int g = hd.g, h0 = hd.h0, b = hd.b;
       const bool new_q = starts;
       starts = ++j == pc.b;
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
       const int s = cnt % NST;
       const bool ok = mbar_wait(smem_u32(&empty[s]), ((cnt / NST) & 1u) ^ 1u, abort_flag, kWaitDecodeEmpty, err);
       if (!__all_sync(0xffffffffu, ok)) break;
+      cur.valid = paged_valid(a, cur);
       const uint32_t live = __ballot_sync(0xffffffffu, cur.valid > 0);
       if (!is_k && lane < MAX_SLOTS) sm.nvalid[s][lane] = cur.valid;
       __syncwarp();
@@ -610,8 +612,7 @@ static cudaError_t launch_paged_tc(const PagedDecodeArgs& a, cudaStream_t st) {
     raised.fetch_or(bit, std::memory_order_relaxed);
   }
   const int grid = num_sms() < kPagedMaxCtas ? num_sms() : kPagedMaxCtas;
-  kern<<<grid, pdt::THREADS, smem, st>>>(tq, tk, tv, a, maps);
-  return cudaGetLastError();
+  return paged_launch(kern, grid, pdt::THREADS, smem, st, tq, tk, tv, a, maps);
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeArgs& args, cudaStream_t st) {

@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
   __shared__ SimtSmem<G, D> sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = lane >> 4, l16 = lane & 15;
   const PagedRows rows = paged_rows(a);
+  paged_begin();
   const int mine = paged_first_tiles(a);
   const PagedRun run = paged_run<THREADS>(a, sm.run, mine, SEG_COST, PARTS_PER_TILE);
   paged_empty_rows(a, tid, THREADS);
@@ -85,7 +86,8 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
     for (int t = pc.a; t < pc.b; ++t) {
       // this half-warp's 8 consecutive keys lie in one page (pages hold at least 8 tokens)
       const int k0 = t * kPagedTile + (warp * 2 + half) * KPW;
-      const PagedSpan sp = paged_span(a, hd.b, hd.g, len, k0, KPW);
+      PagedSpan sp = paged_span(a, hd.b, hd.g, len, k0, KPW);
+      sp.valid = paged_valid(a, sp);
       const size_t base = (size_t)max(sp.page, 0) * a.pool.page + (size_t)sp.in_page * a.pool.token +
                           (size_t)hd.g * a.pool.head;
       const float* kr = static_cast<const float*>(a.k) + base;
@@ -196,11 +198,8 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
 template <int G>
 static cudaError_t launch_simt(const PagedDecodeArgs& a, cudaStream_t st) {
   const int grid = min(num_sms(), kPagedMaxCtas);
-  if (a.D == 64)
-    paged_decode_simt_kernel<G, 64><<<grid, pds::THREADS, 0, st>>>(a);
-  else
-    paged_decode_simt_kernel<G, 128><<<grid, pds::THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+  if (a.D == 64) return paged_launch(paged_decode_simt_kernel<G, 64>, grid, pds::THREADS, 0, st, a);
+  return paged_launch(paged_decode_simt_kernel<G, 128>, grid, pds::THREADS, 0, st, a);
 }
 
 cudaError_t launch_paged_decode_simt(const PagedDecodeArgs& args, cudaStream_t st) {

@@ -11,7 +11,7 @@
 #include <math_constants.h>
 
 #include "kernels.h"
-#include "paged.h"
+#include "paged.cuh"
 
 namespace ra {
 
@@ -58,6 +58,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
 
 template <typename T>
 __global__ void __launch_bounds__(pgb::THREADS) page_bounds_kernel(BoundsArgs a) {
+  paged_begin();
   const int b = blockIdx.y, ps = 1 << a.ps_log2;
   const int len = min(max(a.seq_lens[b], 0), a.W << a.ps_log2);
   const int start = a.start_lens ? max(a.start_lens[b], 0) : 0;
@@ -97,11 +98,8 @@ cudaError_t launch_page_bounds(const BoundsArgs& a, cudaStream_t st) {
   // enough blocks to fill the GPU; each walks its share of a sequence's pages
   const int gx = max(1, min(a.W, num_sms() * 16 / a.B));
   const dim3 grid(gx, a.B);
-  if (a.elem_bytes == 2)
-    page_bounds_kernel<__nv_bfloat16><<<grid, pgb::THREADS, 0, st>>>(a);
-  else
-    page_bounds_kernel<float><<<grid, pgb::THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+  if (a.elem_bytes == 2) return paged_launch(page_bounds_kernel<__nv_bfloat16>, grid, pgb::THREADS, 0, st, a);
+  return paged_launch(page_bounds_kernel<float>, grid, pgb::THREADS, 0, st, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -122,6 +120,7 @@ __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162floa
 template <typename T, int D>
 __global__ void __launch_bounds__(pgsc::THREADS) page_scores_kernel(ScoresArgs a, int G) {
   extern __shared__ float sq[];    // [G][D]
+  paged_begin();
   const int g = blockIdx.y % a.Hkv, b = blockIdx.y / a.Hkv;
   const int ps = 1 << a.ps_log2;
   const int len = min(max(a.seq_lens[b], 0), a.W << a.ps_log2);
@@ -164,10 +163,7 @@ cudaError_t launch_page_scores(const ScoresArgs& a, bool bf16, cudaStream_t st) 
   const int gx = max(1, min((a.W + 7) / 8, num_sms() * 8 / rows));
   const dim3 grid(gx, rows);
   const size_t smem = (size_t)G * a.D * sizeof(float);
-  auto go = [&](auto kern) -> cudaError_t {
-    kern<<<grid, pgsc::THREADS, smem, st>>>(a, G);
-    return cudaGetLastError();
-  };
+  auto go = [&](auto kern) -> cudaError_t { return paged_launch(kern, grid, pgsc::THREADS, smem, st, a, G); };
   if (bf16) return a.D == 64 ? go(page_scores_kernel<__nv_bfloat16, 64>) : go(page_scores_kernel<__nv_bfloat16, 128>);
   return a.D == 64 ? go(page_scores_kernel<float, 64>) : go(page_scores_kernel<float, 128>);
 }
@@ -198,6 +194,7 @@ __global__ void __launch_bounds__(pgse::THREADS) page_select_kernel(SelectArgs a
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
   __shared__ uint32_t s_warp[NW];
+  paged_begin();
   const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = row / a.Hkv, ps = 1 << a.ps_log2;
   const int len = min(max(a.seq_lens[b], 0), a.W << a.ps_log2);
@@ -263,8 +260,7 @@ __global__ void __launch_bounds__(pgse::THREADS) page_select_kernel(SelectArgs a
 }
 
 cudaError_t launch_page_select(const SelectArgs& a, cudaStream_t st) {
-  page_select_kernel<<<a.B * a.Hkv, pgse::THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+  return paged_launch(page_select_kernel, a.B * a.Hkv, pgse::THREADS, 0, st, a);
 }
 
 }  // namespace ra

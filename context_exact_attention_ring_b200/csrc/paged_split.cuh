@@ -16,8 +16,7 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
-#include "paged.h"
-#include "ptx.cuh"
+#include "paged.cuh"
 
 namespace ra {
 
@@ -40,6 +39,11 @@ __device__ __forceinline__ int paged_keys(const PagedDecodeArgs& a, int r) {
 __device__ __forceinline__ int paged_tiles(const PagedDecodeArgs& a, int r) {
   return (paged_keys(a, r) + kPagedTile - 1) / kPagedTile;
 }
+
+// Segments of up to this many tiles are not split: the CTA that has their
+// first unit takes them whole.  Joining costs some 5 us at the end of a call
+// (partial results to L2, an atomic, the parts back), four tiles 3 us.
+constexpr int kPagedWhole = 4;
 
 // Units of work of a row's segments: its tiles, and what starting and
 // finishing a segment costs, in tiles (a run's boundary in that tail belongs
@@ -186,11 +190,12 @@ struct PagedWalk {
       p.sub = o / nu;
       p.nt = nt;
       p.a = o - p.sub * nu;
-      const int end = min(nu, p.a + (t1 - t));
-      p.b = min(nt, end);
+      const bool whole = nt <= kPagedWhole;
+      const int end = whole ? nu : min(nu, p.a + (t1 - t));
+      p.b = whole && p.a > 0 ? 0 : min(nt, end);
       p.seg_t = row_t + p.sub * nu;
       t += end - p.a;
-      if (p.a < p.b) return true;    // else only the tail of a segment
+      if (p.a < p.b) return true;    // else the tail of a segment, or the rest of one that is not split
     }
     return false;
   }
@@ -208,7 +213,7 @@ __device__ __forceinline__ PagedHead paged_head(const PagedDecodeArgs& a, int ro
     grp = sub;
   } else {
     p.b = row;
-    p.g = sub / a.ngrp;
+    p.g = a.ngrp == 1 ? sub : sub / a.ngrp;
     grp = sub - p.g * a.ngrp;
   }
   p.h0 = p.g * a.G + grp * group_heads;
@@ -219,7 +224,8 @@ __device__ __forceinline__ PagedHead paged_head(const PagedDecodeArgs& a, int ro
 // Pool page and number of valid keys of the keys [k0, k0 + n) of a segment
 // (n divides the page size or the reverse; the keys lie in one page).  Keys
 // past the length, listed pages outside the sequence and table entries
-// outside the pool have no valid key.
+// outside the pool have no valid key; the last is left to paged_valid, so that
+// the table entry may be on its way meanwhile.
 struct PagedSpan {
   int page, in_page, valid;
 };
@@ -236,11 +242,11 @@ __device__ __forceinline__ PagedSpan paged_span(const PagedDecodeArgs& a, int b,
     if (lp < 0 || lp >= a.W) return s;
   }
   s.valid = min(max(len - (lp << a.ps_log2) - s.in_page, 0), n);
-  if (s.valid > 0) {
-    s.page = a.table[(size_t)b * a.table_stride + lp];
-    if (s.page < 0 || s.page >= a.num_pages) s.valid = 0;
-  }
+  if (s.valid > 0) s.page = a.table[(size_t)b * a.table_stride + lp];
   return s;
+}
+__device__ __forceinline__ int paged_valid(const PagedDecodeArgs& a, const PagedSpan& s) {
+  return (unsigned)s.page < (unsigned)a.num_pages ? s.valid : 0;
 }
 
 __device__ __forceinline__ void paged_store(const PagedDecodeArgs& a, size_t at, float x) {

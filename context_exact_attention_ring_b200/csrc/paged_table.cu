@@ -17,8 +17,7 @@
 #include <cuda_runtime.h>
 
 #include "kernels.h"
-#include "paged.h"
-#include "ptx.cuh"
+#include "paged.cuh"
 
 namespace ra {
 
@@ -80,6 +79,7 @@ __global__ void __launch_bounds__(pgt::THREADS, 1) page_extend_kernel(ExtendArgs
   __shared__ long long s_warp[NW];
   __shared__ int s_old[THREADS], s_need[THREADS];
   __shared__ long long s_off[THREADS];
+  paged_begin();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long cap = (long long)a.W << a.ps_log2;
   const int n_free = min(max(*a.n_free, 0), a.max_free);
@@ -126,17 +126,16 @@ __global__ void __launch_bounds__(pgt::THREADS, 1) page_extend_kernel(ExtendArgs
 }
 
 __global__ void __launch_bounds__(256) slot_map_kernel(ExtendArgs a) {
+  paged_begin();
   const int t = blockIdx.x * 256 + threadIdx.x;
   if (t < a.max_tokens) a.slot_map[t] = slot_of(a, t);
 }
 
 cudaError_t launch_page_extend(const ExtendArgs& a, cudaStream_t st) {
   const int one = a.max_tokens <= pgt::ONE_LAUNCH_TOKENS;
-  page_extend_kernel<<<1, pgt::THREADS, 0, st>>>(a, one);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = paged_launch(page_extend_kernel, 1, pgt::THREADS, 0, st, a, one);
   if (e != cudaSuccess || one) return e;
-  slot_map_kernel<<<(a.max_tokens + 255) / 256, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return paged_launch(slot_map_kernel, (a.max_tokens + 255) / 256, 256, 0, st, a);
 }
 
 __global__ void __launch_bounds__(pgt::THREADS, 1) page_trim_kernel(TrimArgs a) {
@@ -144,6 +143,7 @@ __global__ void __launch_bounds__(pgt::THREADS, 1) page_trim_kernel(TrimArgs a) 
   __shared__ long long s_warp[NW];
   __shared__ int s_from[THREADS], s_gone[THREADS];
   __shared__ long long s_off[THREADS];
+  paged_begin();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long cap = (long long)a.W << a.ps_log2;
   const int n_free = min(max(*a.n_free, 0), a.max_free);
@@ -189,8 +189,7 @@ __global__ void __launch_bounds__(pgt::THREADS, 1) page_trim_kernel(TrimArgs a) 
 }
 
 cudaError_t launch_page_trim(const TrimArgs& a, cudaStream_t st) {
-  page_trim_kernel<<<1, pgt::THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+  return paged_launch(page_trim_kernel, 1, pgt::THREADS, 0, st, a);
 }
 
 }  // namespace ra
