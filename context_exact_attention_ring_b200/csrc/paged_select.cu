@@ -16,151 +16,232 @@
 namespace ra {
 
 // ---------------------------------------------------------------------------
-// bounds.  A copy-like pass over the keys: a block takes one page at a time of
-// one sequence, a thread a 4-element column of the page's rows of all heads.
+// bounds.  Bound by the bytes of the keys: a thread takes a 16-byte column of
+// a page's rows (all heads of a token are neighbours in the usual layout, so
+// a page is read in whole lines), 8 rows in flight.  The columns of all pages
+// of a sequence are numbered through, so that pages of few heads fill blocks
+// as well.  bf16 pairs are compared two at a time.
 // ---------------------------------------------------------------------------
 namespace pgb {
 constexpr int THREADS = 256;
 }
 
-// minimum and maximum that keep a NaN
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  x[0] = __uint_as_float(v.x << 16);
-  x[1] = __uint_as_float(v.x & 0xffff0000u);
-  x[2] = __uint_as_float(v.y << 16);
-  x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-// exact: the values came from bf16
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
-  *reinterpret_cast<uint2*>(p) =
-      make_uint2((__float_as_uint(x[0]) >> 16) | (__float_as_uint(x[1]) & 0xffff0000u),
-                 (__float_as_uint(x[2]) >> 16) | (__float_as_uint(x[3]) & 0xffff0000u));
-}
+// four 32-bit words of float or of two bf16 each: minimum / maximum that keep a NaN
+template <typename T>
+struct Word;
+template <>
+struct Word<float> {
+  static constexpr uint32_t MAX = 0x7f800000u, MIN = 0xff800000u;   // +inf, -inf
+  __device__ __forceinline__ static uint32_t lo(uint32_t a, uint32_t b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+    return __float_as_uint(r);
+  }
+  __device__ __forceinline__ static uint32_t hi(uint32_t a, uint32_t b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+    return __float_as_uint(r);
+  }
+};
+template <>
+struct Word<__nv_bfloat16> {
+  static constexpr uint32_t MAX = 0x7f807f80u, MIN = 0xff80ff80u;
+  __device__ __forceinline__ static uint32_t lo(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ __forceinline__ static uint32_t hi(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+};
 
 template <typename T>
 __global__ void __launch_bounds__(pgb::THREADS) page_bounds_kernel(BoundsArgs a) {
   paged_begin();
+  constexpr int E = 16 / sizeof(T);      // elements of a column
+  constexpr int U = 8;                   // rows in flight (pages hold at least 8)
   const int b = blockIdx.y, ps = 1 << a.ps_log2;
   const int len = min(max(a.seq_lens[b], 0), a.W << a.ps_log2);
-  const int start = a.start_lens ? max(a.start_lens[b], 0) : 0;
+  const int p0 = (a.start_lens ? max(a.start_lens[b], 0) : 0) >> a.ps_log2;
   const int np = (len + ps - 1) >> a.ps_log2;
-  const int nc = a.Hkv * a.D / 4;
-  for (int p = (start >> a.ps_log2) + blockIdx.x; p < np; p += gridDim.x) {
+  const int nc = a.Hkv * a.D / E, step = gridDim.x * pgb::THREADS;
+  const int dp = step / nc, dc = step - dp * nc;
+  int p = p0 + (blockIdx.x * pgb::THREADS + threadIdx.x) / nc;
+  int c = (blockIdx.x * pgb::THREADS + threadIdx.x) % nc;
+  for (; p < np; p += dp, c += dc) {
+    if (c >= nc) {
+      c -= nc;
+      if (++p >= np) break;
+    }
     const int page = a.table[(size_t)b * a.table_stride + p];
     if (page < 0 || page >= a.num_pages) continue;
     const int rows = min(ps, len - (p << a.ps_log2));
-    for (int c = threadIdx.x; c < nc; c += pgb::THREADS) {
-      const int h = c * 4 / a.D, d = c * 4 - h * a.D;
-      const T* k = static_cast<const T*>(a.k) + (long long)page * a.pool.page + (long long)h * a.pool.head + d;
-      float lo[4], hi[4];
+    const int h = c * E / a.D, d = c * E - h * a.D;
+    const T* k = static_cast<const T*>(a.k) + (long long)page * a.pool.page + (long long)h * a.pool.head + d;
+    uint32_t lo[4], hi[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[i] = CUDART_INF_F;
-        hi[i] = -CUDART_INF_F;
-      }
-#pragma unroll 8
-      for (int r = 0; r < rows; ++r) {
-        float x[4];
-        load4(k + (long long)r * a.pool.token, x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          lo[i] = min_nan(lo[i], x[i]);
-          hi[i] = max_nan(hi[i], x[i]);
-        }
-      }
-      T* o = static_cast<T*>(a.bounds) + ((long long)page * a.Hkv + h) * 2 * a.D + d;
-      store4(o, lo);
-      store4(o + a.D, hi);
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = Word<T>::MAX;
+      hi[i] = Word<T>::MIN;
     }
+    auto take = [&](const uint4& x) {
+      lo[0] = Word<T>::lo(lo[0], x.x); hi[0] = Word<T>::hi(hi[0], x.x);
+      lo[1] = Word<T>::lo(lo[1], x.y); hi[1] = Word<T>::hi(hi[1], x.y);
+      lo[2] = Word<T>::lo(lo[2], x.z); hi[2] = Word<T>::hi(hi[2], x.z);
+      lo[3] = Word<T>::lo(lo[3], x.w); hi[3] = Word<T>::hi(hi[3], x.w);
+    };
+    for (int r = 0; r < rows; r += U) {
+      // past the last valid row that row again: it changes nothing
+      uint4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        x[u] = *reinterpret_cast<const uint4*>(k + (long long)min(r + u, rows - 1) * a.pool.token);
+#pragma unroll
+      for (int u = 0; u < U; ++u) take(x[u]);
+    }
+    T* o = static_cast<T*>(a.bounds) + ((long long)page * a.Hkv + h) * 2 * a.D + d;
+    *reinterpret_cast<uint4*>(o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(o + a.D) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   }
 }
 
 cudaError_t launch_page_bounds(const BoundsArgs& a, cudaStream_t st) {
-  // enough blocks to fill the GPU; each walks its share of a sequence's pages
-  const int gx = max(1, min(a.W, num_sms() * 16 / a.B));
-  const dim3 grid(gx, a.B);
+  // enough blocks to fill the GPU, no more than a sequence's table has columns
+  const long long cols = (long long)a.W * (a.Hkv * a.D * a.elem_bytes / 16);
+  const long long most = (cols + pgb::THREADS - 1) / pgb::THREADS;
+  const int fill = max(1, num_sms() * 16 / a.B);
+  const dim3 grid((unsigned)(most < fill ? most : fill), a.B);
   if (a.elem_bytes == 2) return paged_launch(page_bounds_kernel<__nv_bfloat16>, grid, pgb::THREADS, 0, st, a);
   return paged_launch(page_bounds_kernel<float>, grid, pgb::THREADS, 0, st, a);
 }
 
 // ---------------------------------------------------------------------------
-// scores.  Bound by the bytes of the bounds: a warp takes a page, a lane D/32
-// of its dims; the group's queries wait in shared memory.
+// scores.  Bound by the bytes of the bounds.  A half-warp shares a page, 8 (or
+// 4) dims a lane in 16-byte pieces, and holds four pages at once; the group's
+// queries wait in shared memory, so that any number of heads takes one pass.
+// max(q lo, q hi) is q times hi or lo by the sign of q: a select and an FMA.
+// The four pages' sums are added up across the half-warp by halving: after two
+// exchanges a lane has one page, in six shuffles instead of sixteen.
 // ---------------------------------------------------------------------------
 namespace pgsc {
 constexpr int THREADS = 256;
-}
+constexpr int U = 4;                              // pages of a half-warp
+constexpr int PPB = THREADS / 16 * U;             // pages of a block at a time
+}  // namespace pgsc
 
-template <typename T>
-__device__ __forceinline__ float widen(T x);
-template <>
+// the N = D / 16 elements of lane l of 16, in pieces of 16 bytes
+template <typename T, int D>
+struct Sixteenth {
+  static constexpr int N = D / 16;
+  static constexpr int E = N * sizeof(T) < 16 ? N : 16 / sizeof(T);    // elements of a piece
+  __device__ __forceinline__ static int dim(int l, int i) { return (i / E) * 16 * E + l * E + i % E; }
+  __device__ __forceinline__ static void load(const T* row, int l, float (&x)[N]) {
+#pragma unroll
+    for (int j = 0; j < N / E; ++j) {
+      const T* at = row + j * 16 * E + l * E;
+      if constexpr (sizeof(T) == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(at);
+        x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
+      } else {
+        uint32_t w[E / 2];
+        if constexpr (E == 8) {
+          const uint4 v = *reinterpret_cast<const uint4*>(at);
+          w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(at);
+          w[0] = v.x; w[1] = v.y;
+        }
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          x[2 * i] = __uint_as_float(w[i] << 16);
+          x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+      }
+    }
+  }
+};
+
 __device__ __forceinline__ float widen(float x) { return x; }
-template <>
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(pgsc::THREADS) page_scores_kernel(ScoresArgs a, int G) {
-  extern __shared__ float sq[];    // [G][D]
+  using namespace pgsc;
+  using Row = Sixteenth<T, D>;
+  constexpr int N = Row::N;
+  extern __shared__ __align__(16) float sq[];    // [G][16][N]: lane l's dims together
   paged_begin();
   const int g = blockIdx.y % a.Hkv, b = blockIdx.y / a.Hkv;
   const int ps = 1 << a.ps_log2;
   const int len = min(max(a.seq_lens[b], 0), a.W << a.ps_log2);
   const int np = (len + ps - 1) >> a.ps_log2;
   const T* q = static_cast<const T*>(a.q) + b * a.q_b + (long long)g * G * a.q_h;
-  for (int e = threadIdx.x; e < G * D; e += pgsc::THREADS) sq[e] = widen(q[(long long)(e / D) * a.q_h + e % D]);
+  for (int e = threadIdx.x; e < G * D; e += THREADS) {
+    const int h = e / D, l = e % D / N, i = e % N;
+    sq[e] = widen(q[(long long)h * a.q_h + Row::dim(l, i)]);
+  }
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int N = D / 32, NW = pgsc::THREADS / 32;
+  const int lane = threadIdx.x & 31, l = lane & 15;
+  const bool b1 = l & 8, b0 = l & 4;
+  const int mine = (b1 ? 2 : 0) + (b0 ? 1 : 0);
   float* out = a.scores + (size_t)blockIdx.y * a.W;
-  for (int p = blockIdx.x * NW + warp; p < a.W; p += gridDim.x * NW) {
-    float best = -CUDART_INF_F;
-    const int page = p < np ? a.table[(size_t)b * a.table_stride + p] : -1;
-    if (page >= 0 && page < a.num_pages) {
-      const T* x = static_cast<const T*>(a.bounds) + ((long long)page * a.Hkv + g) * 2 * D + lane * N;
-      float lo[N], hi[N];
+  const int32_t* table = a.table + (size_t)b * a.table_stride;
+  for (int p0 = blockIdx.x * PPB; p0 < a.W; p0 += gridDim.x * PPB) {
+    const int first = p0 + threadIdx.x / 16 * U;
+    float lo[U][N], hi[U][N];
+    uint32_t live = 0;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        lo[i] = widen(x[i]);
-        hi[i] = widen(x[D + i]);
-      }
-      for (int h = 0; h < G; ++h) {
-        float s = 0.f;
+    for (int u = 0; u < U; ++u) {
+      const int page = first + u < np ? table[first + u] : -1;
+      const bool ok = page >= 0 && page < a.num_pages;
+      live |= (uint32_t)ok << u;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float qd = sq[h * D + lane * N + i];
-          s += fmaxf(qd * lo[i], qd * hi[i]);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        best = h ? max(best, s) : s;
+      for (int i = 0; i < N; ++i) lo[u][i] = hi[u][i] = 0.f;
+      if (ok) {
+        const T* x = static_cast<const T*>(a.bounds) + ((long long)page * a.Hkv + g) * 2 * D;
+        Row::load(x, l, lo[u]);
+        Row::load(x + D, l, hi[u]);
       }
     }
-    if (lane == 0) out[p] = best;
+    if (__any_sync(0xffffffffu, live != 0)) {
+      float best = -CUDART_INF_F;
+      bool nan = false;
+      for (int h = 0; h < G; ++h) {
+        float qd[N], s[U];
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j)
+          *reinterpret_cast<float4*>(qd + 4 * j) = *reinterpret_cast<const float4*>(sq + h * D + l * N + 4 * j);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          s[u] = 0.f;
+#pragma unroll
+          for (int i = 0; i < N; ++i) s[u] = fmaf(qd[i], qd[i] < 0.f ? lo[u][i] : hi[u][i], s[u]);
+        }
+        // keep two pages and send the others' sums, then one
+        float s0 = b1 ? s[2] : s[0], s1 = b1 ? s[3] : s[1];
+        s0 += __shfl_xor_sync(0xffffffffu, b1 ? s[0] : s[2], 8);
+        s1 += __shfl_xor_sync(0xffffffffu, b1 ? s[1] : s[3], 8);
+        float x = b0 ? s1 : s0;
+        x += __shfl_xor_sync(0xffffffffu, b0 ? s0 : s1, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        nan |= x != x;
+        best = fmaxf(best, x);
+      }
+      if (nan) best = CUDART_NAN_F;
+      if ((l & 3) == 0 && first + mine < a.W) out[first + mine] = live >> mine & 1 ? best : -CUDART_INF_F;
+    } else if ((l & 3) == 0 && first + mine < a.W) {
+      out[first + mine] = -CUDART_INF_F;
+    }
   }
 }
 
 cudaError_t launch_page_scores(const ScoresArgs& a, bool bf16, cudaStream_t st) {
   const int G = a.Hq / a.Hkv, rows = a.B * a.Hkv;
-  const int gx = max(1, min((a.W + 7) / 8, num_sms() * 8 / rows));
+  const int gx = max(1, min((a.W + pgsc::PPB - 1) / pgsc::PPB, num_sms() * 8 / rows));
   const dim3 grid(gx, rows);
   const size_t smem = (size_t)G * a.D * sizeof(float);
   auto go = [&](auto kern) -> cudaError_t { return paged_launch(kern, grid, pgsc::THREADS, smem, st, a, G); };
@@ -170,32 +251,59 @@ cudaError_t launch_page_scores(const ScoresArgs& a, bool bf16, cudaStream_t st) 
 
 // ---------------------------------------------------------------------------
 // selection.  A block per (sequence, kv head).  Scores become 32-bit keys of
-// the same order; four passes of 8 bits each narrow down the K-th largest key,
-// and one ordered pass writes the pages above it and the first ones equal to
-// it.
+// the same order, kept in shared memory 8192 at a time; three passes of 11,
+// 11 and 10 bits narrow down the K-th largest key (a histogram of 2048 bins
+// keeps the atomics apart, and the block sums it from the top), and one ordered pass writes the
+// pages above it and the first ones equal to it.  Latency-bound: a list is a
+// few KB.
 // ---------------------------------------------------------------------------
 namespace pgse {
 constexpr int THREADS = 1024;
 constexpr int NW = THREADS / 32;
+constexpr int TILE = 8192;             // keys in shared memory
+constexpr int BINS = 2048;
 }  // namespace pgse
 
 // Order-preserving key: pages that are always kept first, then NaN, then by value (-0 equal to 0).
-__device__ __forceinline__ uint32_t select_key(const SelectArgs& a, const float* x, int i, int np) {
+__device__ __forceinline__ uint32_t select_key(const SelectArgs& a, float v, int i, int np) {
   if (i < a.keep_first || i >= np - a.keep_last) return 0xffffffffu;
-  const float v = x[i];
   if (v != v) return 0xfffffffeu;
   const uint32_t u = __float_as_uint(v + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(pgse::THREADS) page_select_kernel(SelectArgs a) {
+// Exclusive prefix sum over the block (ends with every thread past its reads of s_warp).
+__device__ __forceinline__ uint32_t select_scan(uint32_t x, uint32_t* s_warp, uint32_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  uint32_t w = s_warp[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t up = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += up;
+  }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const uint32_t before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+  __syncthreads();
+  return incl - x + (warp ? before : 0u);
+}
+
+__global__ void __launch_bounds__(pgse::THREADS, 1) page_select_kernel(SelectArgs a) {
   using namespace pgse;
-  __shared__ int hist[256];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
+  __shared__ uint32_t s_key[TILE];
+  __shared__ int hist[BINS];
   __shared__ uint32_t s_warp[NW];
+  __shared__ uint32_t s_digit;
+  __shared__ int s_need;
   paged_begin();
-  const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = blockIdx.x, tid = threadIdx.x;
   const int b = row / a.Hkv, ps = 1 << a.ps_log2;
   const int len = min(max(a.seq_lens[b], 0), a.W << a.ps_log2);
   const int np = (len + ps - 1) >> a.ps_log2;
@@ -208,54 +316,80 @@ __global__ void __launch_bounds__(pgse::THREADS) page_select_kernel(SelectArgs a
     for (int i = tid; i < np; i += THREADS) sel[i] = i;
     return;
   }
+  const int ntiles = (np + TILE - 1) / TILE;
+  int held = -1;       // the tile in shared memory
+  auto hold = [&](int t) {
+    if (held == t) return;
+    __syncthreads();   // the tile before has been read
+    const int i0 = t * TILE, m = min(TILE, np - i0);
+#pragma unroll 4
+    for (int i = tid; i < m; i += THREADS) s_key[i] = select_key(a, x[i0 + i], i0 + i, np);
+    held = t;
+    __syncthreads();
+  };
   // the K-th largest key: its top bits so far, and how many of the keys with these top bits are wanted
   uint32_t prefix = 0;
   int need = a.K;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t digit_mask = pass == 2 ? 1023u : 2047u;
+    for (int i = tid; i < BINS; i += THREADS) hist[i] = 0;
     __syncthreads();
-    for (int i = tid; i < np; i += THREADS) {
-      const uint32_t k = select_key(a, x, i, np);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
+    for (int t = 0; t < ntiles; ++t) {
+      hold(t);
+      const int m = min(TILE, np - t * TILE);
+      for (int i = tid; i < m; i += THREADS) {
+        const uint32_t k = s_key[i];
+        const bool in = pass == 0 || (k >> (shift + (pass == 2 ? 10 : 11))) == (prefix >> (shift + (pass == 2 ? 10 : 11)));
+        if (in) atomicAdd(&hist[(k >> shift) & digit_mask], 1);
+      }
     }
     __syncthreads();
-    if (tid == 0) {
-      int left = need, d = 255;
-      while (d > 0 && hist[d] < left) left -= hist[d--];
-      s_prefix = prefix | ((uint32_t)d << shift);
-      s_need = left;
+    // thread t holds bins 2047 - 2t and 2046 - 2t; `above` keys lie in higher bins
+    const int hi = hist[BINS - 1 - 2 * tid], lo = hist[BINS - 2 - 2 * tid];
+    uint32_t total;
+    const int above = (int)select_scan((uint32_t)(hi + lo), s_warp, &total);
+    if (above < need && need <= above + hi + lo) {
+      const bool upper = need <= above + hi;
+      s_digit = (uint32_t)(upper ? BINS - 1 - 2 * tid : BINS - 2 - 2 * tid);
+      s_need = need - above - (upper ? 0 : hi);
     }
     __syncthreads();
-    prefix = s_prefix;
+    prefix |= s_digit << shift;
     need = s_need;
   }
-  // keys above `prefix`, and the first `need` equal to it, in index order
-  int above = 0, equal = 0;      // before this chunk
-  for (int i0 = 0; i0 < np; i0 += THREADS) {
-    const int i = i0 + tid;
-    const uint32_t k = i < np ? select_key(a, x, i, np) : 0u;
-    const bool gt = i < np && k > prefix, eq = i < np && k == prefix;
-    const uint32_t mine = (gt ? 1u : 0u) | (eq ? 0x10000u : 0u);
-    uint32_t incl = mine;
+  // keys above `prefix`, and the first `need` equal to it, in index order: a thread takes 8 in a row
+  int above = 0, equal = 0;      // before this tile
+  for (int t = 0; t < ntiles; ++t) {
+    hold(t);
+    constexpr int PER = TILE / THREADS;
+    const int m = min(TILE, np - t * TILE);
+    uint32_t mine = 0;           // keys equal to prefix : keys above it
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
+    for (int i = 0; i < PER; ++i) {
+      const int at = tid * PER + i;
+      const uint32_t k = at < m ? s_key[at] : 0u;
+      mine += (at < m && k > prefix ? 1u : 0u) + (at < m && k == prefix ? 0x10000u : 0u);
     }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    uint32_t before = 0, chunk = 0;
+    uint32_t total;
+    const uint32_t before = select_scan(mine, s_warp, &total);
+    int rg = above + (int)(before & 0xffffu), re = equal + (int)(before >> 16);
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      if (w < warp) before += s_warp[w];
-      chunk += s_warp[w];
+    for (int i = 0; i < PER; ++i) {
+      const int at = tid * PER + i;
+      if (at >= m) break;
+      const uint32_t k = s_key[at];
+      if (k > prefix) {
+        sel[rg + min(re, need)] = t * TILE + at;
+        ++rg;
+      } else if (k == prefix) {
+        if (re < need) sel[rg + re] = t * TILE + at;
+        ++re;
+      }
     }
-    const uint32_t excl = before + incl - mine;
-    const int rg = above + (int)(excl & 0xffffu), re = equal + (int)(excl >> 16);
-    if (gt || (eq && re < need)) sel[rg + min(re, need)] = i;
-    above += (int)(chunk & 0xffffu);
-    equal += (int)(chunk >> 16);
-    __syncthreads();
+    above += (int)(total & 0xffffu);
+    equal += (int)(total >> 16);
   }
 }
 
