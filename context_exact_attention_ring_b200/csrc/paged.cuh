@@ -14,4 +14,11 @@ __device__ __forceinline__ void paged_begin() {
   grid_dependency_wait();
 }
 
+// Maximum over the warp's lanes (NaN ignored, as fmaxf does).
+__device__ __forceinline__ float warp_max_redux(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 }  // namespace ra

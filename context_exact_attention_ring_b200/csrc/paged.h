@@ -8,6 +8,7 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -29,6 +30,20 @@ inline cudaError_t paged_launch(void (*kern)(P...), dim3 grid, int threads, size
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
+// Raises a kernel's shared-memory limit to kBytes, once per device.
+template <int kBytes, typename Kern>
+inline cudaError_t paged_raise_smem(Kern kern) {
+  static std::atomic<const void*> raised[64];    // of every instantiation's type; a kernel is told by its address
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const void* k = reinterpret_cast<const void*>(kern);
+  if (dev < 64 && raised[dev].load(std::memory_order_relaxed) == k) return cudaSuccess;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e == cudaSuccess && dev < 64) raised[dev].store(k, std::memory_order_relaxed);
+  return e;
 }
 
 struct PoolStrides {

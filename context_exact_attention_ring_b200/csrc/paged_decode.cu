@@ -34,7 +34,6 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "kernels.h"
@@ -137,13 +136,6 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
-}
-
-// Maximum over the warp's lanes (NaN ignored, as fmaxf does).
-__device__ __forceinline__ float warp_max_redux(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
 }
 
 template <int G, int DH>
@@ -597,20 +589,11 @@ static cudaError_t launch_paged_tc(const PagedDecodeArgs& a, cudaStream_t st) {
               : paged_map(m, base, DH, {a.Hkv, ps, a.num_pages}, {p.head, p.token, p.page}, {1, rows, 1})))
       return cudaErrorInvalidValue;
   }
-  const size_t smem = sizeof(PagedSmem<G, DH>) + 1024;
+  constexpr int smem = sizeof(PagedSmem<G, DH>) + 1024;
   static_assert(sizeof(PagedSmem<G, DH>) + 1024 <= 232448, "shared memory of a CTA");
   auto kern = paged_decode_kernel<G, DH>;
-  // the shared-memory limit is raised once per device
-  static std::atomic<unsigned long long> raised{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = paged_raise_smem<smem>(kern);
   if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (!(raised.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    raised.fetch_or(bit, std::memory_order_relaxed);
-  }
   const int grid = num_sms() < kPagedMaxCtas ? num_sms() : kPagedMaxCtas;
   return paged_launch(kern, grid, pdt::THREADS, smem, st, tq, tk, tv, a, maps);
 }

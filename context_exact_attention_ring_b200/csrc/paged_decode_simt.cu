@@ -1,154 +1,161 @@
-// Paged decode on CUDA cores: one new token per sequence against the keys in
-// its cache pages,
+// Paged decode on CUDA cores (float32 cache): one new token per sequence
+// against the keys in its cache pages,
 //   out_h = sum_j softmax_j(scale q_h . k_j) v_j,   lse_h = ln sum_j e^(scale q_h . k_j),
-// in one pass over the keys with a running maximum and sum.
+// in one pass over the keys with a running maximum and sum.  The tensor cores
+// have no float32 product; every product and sum here is float32.
 //
-// float32 caches run here (the tensor cores have no float32 product); every
-// product and sum is float32.  A CTA of 8 warps takes the tiles of its run
-// (paged_split.cuh) 128 keys at a time, 16 keys a warp: 16 lanes share a key
-// row, so that a row is one contiguous load of the half-warp, and each lane
-// keeps D/16 dims of the queries and outputs of up to 8 heads in registers.
+// A CTA of 16 warps takes the tiles of its run (paged_split.cuh), 8 keys a
+// warp.  D / 4 lanes share a key row (one contiguous load), and each lane keeps
+// 4 dims of the outputs of up to 8 heads in registers, as packed pairs.  Four keys go through at once: their partial scores are added up
+// across the lanes by halving (2 + 1 exchanges leave a lane one key, the rest
+// are plain), so that a lane ends with one score and takes one exponential per
+// head, and the four weights return by shuffles.  Bound by memory for few heads and
+// by instructions for many: about 55 per head and four keys of a warp.
 #include <cuda_runtime.h>
+#include <math_constants.h>
 
 #include "kernels.h"
-#include "paged.h"
 #include "paged_split.cuh"
 
 namespace ra {
 
 namespace pds {
-constexpr int THREADS = 256;
+constexpr int THREADS = 512;
 constexpr int NW = THREADS / 32;
-constexpr int KPW = 8;      // keys a half-warp holds at once (a tile is 8 warps x 2 x 8 keys)
-constexpr int HEADS = 8;    // query heads of a group, at most
-constexpr int SEG_COST = 1;         // what a segment costs besides its tiles, in tiles
-constexpr int PARTS_PER_TILE = 10;  // parts joined in the time of a tile
+constexpr int KPW = kPagedTile / NW;   // keys of a tile a warp takes
+constexpr int HEADS = 8;               // query heads of a group, at most
+constexpr int SEG_COST = 1;            // what a segment costs besides its tiles, in tiles
+constexpr int PARTS_PER_TILE = 10;     // parts joined in the time of a tile
+static_assert(KPW == 8, "a warp's keys lie in one page (pages hold at least 8 tokens)");
 }  // namespace pds
-static_assert(pds::NW * 2 * pds::KPW == kPagedTile, "a CTA takes a tile at a time");
-
-// Dims of a row that lane l (0..15) of a half-warp holds: D/64 pieces of 4,
-// contiguous over the lanes.
-template <int D>
-struct RowPiece {
-  static constexpr int N = D / 16;
-  __device__ __forceinline__ static int dim(int l, int i) { return (i >> 2) * 64 + l * 4 + (i & 3); }
-  __device__ __forceinline__ static void load(const float* row, int l, float (&x)[N]) {
-#pragma unroll
-    for (int j = 0; j < N / 4; ++j) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(row + j * 64 + l * 4));
-      x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
-    }
-  }
-};
 
 template <int G, int D>
 struct SimtSmem {
   PagedRunSmem run;
+  alignas(16) float q[G][D];
+  float m[pds::NW][G], l[pds::NW][G];
+  int last;
   union {
     float o[pds::NW][G][D];
     typename PagedJoin<pds::THREADS, G, D>::Smem join;
   };
-  float m[pds::NW][G], l[pds::NW][G];
-  int last;
 };
 
 template <int G, int D>
 __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(PagedDecodeArgs a) {
   using namespace pds;
-  using Row = RowPiece<D>;
-  constexpr int N = Row::N;
-  __shared__ SimtSmem<G, D> sm;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = lane >> 4, l16 = lane & 15;
-  const PagedRows rows = paged_rows(a);
+  constexpr int LPR = D / 4, RPW = 32 / LPR;      // lanes of a row, rows a warp loads at once
+  constexpr int NB = KPW / (4 * RPW);             // batches of 4 keys per group of lanes
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SimtSmem<G, D>& sm = *reinterpret_cast<SimtSmem<G, D>*>(smem_raw);
   paged_begin();
-  const int mine = paged_first_tiles(a);
-  const PagedRun run = paged_run<THREADS>(a, sm.run, mine, SEG_COST, PARTS_PER_TILE);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = lane / LPR, lr = lane % LPR;
+  const PagedRows rows = paged_rows(a);
+  const PagedRun run = paged_run<THREADS>(a, sm.run, paged_first_tiles(a), SEG_COST, PARTS_PER_TILE);
   paged_empty_rows(a, tid, THREADS);
   const float sl2 = a.scale * 1.4426950408889634f;
+  // after the exchanges a lane holds key `mine` of its group's four
+  const bool b1 = lr & (LPR / 2), b0 = lr & (LPR / 4);
+  const int mine = (b1 ? 2 : 0) + (b0 ? 1 : 0);
   PagedWalk walk(run, SEG_COST);
   PagedPiece pc;
   while (walk.next(a, rows, pc)) {
     const PagedHead hd = paged_head(a, pc.row, pc.sub, HEADS);
     const int len = paged_len(a, hd.b);
-    float q[G][N], acc[G][N], m[G], l[G];
+    // the queries, scaled, in shared memory (free since the barriers of the piece before)
+    for (int e = tid; e < G * D; e += THREADS) {
+      const int h = e / D;
+      sm.q[h][e - h * D] = h < hd.nh ? static_cast<const float*>(a.q)[(size_t)hd.b * a.q_b + (size_t)(hd.h0 + h) * a.q_h +
+                                                                      e - h * D] * sl2
+                                     : 0.f;
+    }
+    uint64_t acc[G][2];
+    float m[G], l[G];
 #pragma unroll
     for (int h = 0; h < G; ++h) {
-      const float* qr = static_cast<const float*>(a.q) + (size_t)hd.b * a.q_b + (size_t)(hd.h0 + (h < hd.nh ? h : 0)) * a.q_h;
-      Row::load(qr, l16, q[h]);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        q[h][i] *= sl2;
-        acc[h][i] = 0.f;
-      }
+      acc[h][0] = acc[h][1] = pack2(0.f, 0.f);
       m[h] = -CUDART_INF_F;
       l[h] = 0.f;
     }
+    __syncthreads();
+    auto span = [&](int t) { return paged_span(a, hd.b, hd.g, len, t * kPagedTile + warp * KPW, KPW); };
+    PagedSpan next = span(pc.a);
     for (int t = pc.a; t < pc.b; ++t) {
-      // this half-warp's 8 consecutive keys lie in one page (pages hold at least 8 tokens)
-      const int k0 = t * kPagedTile + (warp * 2 + half) * KPW;
-      PagedSpan sp = paged_span(a, hd.b, hd.g, len, k0, KPW);
+      PagedSpan sp = next;
+      if (t + 1 < pc.b) next = span(t + 1);
       sp.valid = paged_valid(a, sp);
-      const size_t base = (size_t)max(sp.page, 0) * a.pool.page + (size_t)sp.in_page * a.pool.token +
-                          (size_t)hd.g * a.pool.head;
+      if (sp.valid == 0) continue;                // the same in the whole warp
+      const size_t base = (size_t)sp.page * a.pool.page + (size_t)sp.in_page * a.pool.token +
+                          (size_t)hd.g * a.pool.head + 4 * lr;
       const float* kr = static_cast<const float*>(a.k) + base;
       const float* vr = static_cast<const float*>(a.v) + base;
-#pragma unroll
-      for (int u0 = 0; u0 < KPW; u0 += 4) {
-        float kx[4][N], vx[4][N], s[4][G];
+#pragma unroll 1
+      for (int n = 0; n < NB; ++n) {
+        ulonglong2 kx[4], vx[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          if (u0 + u < sp.valid) {
-            Row::load(kr + (size_t)(u0 + u) * a.pool.token, l16, kx[u]);
-            Row::load(vr + (size_t)(u0 + u) * a.pool.token, l16, vx[u]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) kx[u][i] = vx[u][i] = 0.f;
+          const int key = (n * 4 + u) * RPW + grp;
+          kx[u] = vx[u] = make_ulonglong2(0ull, 0ull);
+          if (key < sp.valid) {
+            kx[u] = __ldg(reinterpret_cast<const ulonglong2*>(kr + (size_t)key * a.pool.token));
+            vx[u] = __ldg(reinterpret_cast<const ulonglong2*>(vr + (size_t)key * a.pool.token));
           }
         }
-        float mx[G];
-#pragma unroll
-        for (int h = 0; h < G; ++h) mx[h] = m[h];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int h = 0; h < G; ++h) {
-            float x = 0.f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) x = fmaf(q[h][i], kx[u][i], x);
-#pragma unroll
-            for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            s[u][h] = u0 + u < sp.valid ? x : -CUDART_INF_F;
-            mx[h] = fmaxf(mx[h], s[u][h]);
-          }
+        const bool valid = (n * 4 + mine) * RPW + grp < sp.valid;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 16));
-          if (mx[h] > m[h]) {     // the same in the whole warp
-            const float alpha = exp2f(m[h] - mx[h]);
-            l[h] *= alpha;
+          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&sm.q[h][4 * lr]);
+          float s[4];
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[h][i] *= alpha;
-            m[h] = mx[h];
+          for (int u = 0; u < 4; ++u) s[u] = hsum2(ffma2(q.x, kx[u].x, fmul2(q.y, kx[u].y)));
+          // keep two keys and send the others' sums, then one
+          float s0 = b1 ? s[2] : s[0], s1 = b1 ? s[3] : s[1];
+          s0 += __shfl_xor_sync(0xffffffffu, b1 ? s[0] : s[2], LPR / 2);
+          s1 += __shfl_xor_sync(0xffffffffu, b1 ? s[1] : s[3], LPR / 2);
+          float x = b0 ? s1 : s0;
+          x += __shfl_xor_sync(0xffffffffu, b0 ? s0 : s1, LPR / 4);
+#pragma unroll
+          for (int o = LPR / 8; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+          if (!valid) x = -CUDART_INF_F;
+          const float mx = warp_max_redux(x);
+          if (mx > m[h]) {                        // the same in the whole warp
+            const float alpha = exp2f(m[h] - mx);
+            const uint64_t al2 = pack2(alpha, alpha);
+            l[h] *= alpha;
+            acc[h][0] = fmul2(acc[h][0], al2);
+            acc[h][1] = fmul2(acc[h][1], al2);
+            m[h] = mx;
           }
+          const float p = x == -CUDART_INF_F ? 0.f : exp2f(x - m[h]);
+          l[h] += p;                              // every key in LPR / 4 lanes
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const float p = s[u][h] == -CUDART_INF_F ? 0.f : exp2f(s[u][h] - m[h]);
-            l[h] += p;
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[h][i] = fmaf(p, vx[u][i], acc[h][i]);
+            const int src = grp * LPR + (u & 2 ? LPR / 2 : 0) + (u & 1 ? LPR / 4 : 0);
+            const float pu = __shfl_sync(0xffffffffu, p, src);
+            const uint64_t p2 = pack2(pu, pu);
+            acc[h][0] = ffma2(p2, vx[u].x, acc[h][0]);
+            acc[h][1] = ffma2(p2, vx[u].y, acc[h][1]);
           }
         }
       }
     }
-    // ---- join the two half-warps, then the warps
+    // ---- the groups of lanes, then the warps
 #pragma unroll
     for (int h = 0; h < G; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 16);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float o = acc[h][i] + __shfl_xor_sync(0xffffffffu, acc[h][i], 16);
-        if (half == 0) sm.o[warp][h][Row::dim(l16, i)] = o;
+      float4 o;
+      unpack2(acc[h][0], o.x, o.y);
+      unpack2(acc[h][1], o.z, o.w);
+      if constexpr (RPW == 2) {
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
+        o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
+        o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 16);
       }
+      // one lane of each key
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], LPR / 2);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], LPR / 4);
+      if (grp == 0) *reinterpret_cast<float4*>(&sm.o[warp][h][4 * lr]) = o;
       if (lane == 0) {
         sm.m[warp][h] = m[h];
         sm.l[warp][h] = l[h];
@@ -189,32 +196,44 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
         if (sm.last) atomicExch(a.ws_count + c0, 0u);    // zero again for the next call
       }
       __syncthreads();
-      if (sm.last)
-        paged_join<THREADS, G, D>(a, run, pc, hd, c0, c1, tid, sm.join, [] { __syncthreads(); });
+      if (sm.last) paged_join<THREADS, G, D>(a, run, pc, hd, c0, c1, tid, sm.join, [] { __syncthreads(); });
     }
   }
 }
 
+template <int G, int D>
+static cudaError_t launch_simt_gd(const PagedDecodeArgs& a, cudaStream_t st) {
+  auto kern = paged_decode_simt_kernel<G, D>;
+  const cudaError_t e = paged_raise_smem<(int)sizeof(SimtSmem<G, D>)>(kern);
+  if (e != cudaSuccess) return e;
+  return paged_launch(kern, min(num_sms(), kPagedMaxCtas), pds::THREADS, sizeof(SimtSmem<G, D>), st, a);
+}
 template <int G>
 static cudaError_t launch_simt(const PagedDecodeArgs& a, cudaStream_t st) {
-  const int grid = min(num_sms(), kPagedMaxCtas);
-  if (a.D == 64) return paged_launch(paged_decode_simt_kernel<G, 64>, grid, pds::THREADS, 0, st, a);
-  return paged_launch(paged_decode_simt_kernel<G, 128>, grid, pds::THREADS, 0, st, a);
+  return a.D == 64 ? launch_simt_gd<G, 64>(a, st) : launch_simt_gd<G, 128>(a, st);
 }
 
 cudaError_t launch_paged_decode_simt(const PagedDecodeArgs& args, cudaStream_t st) {
   PagedDecodeArgs a = args;
   a.ngrp = (a.G + pds::HEADS - 1) / pds::HEADS;
-  if (a.G == 1) return launch_simt<1>(a, st);
-  if (a.G == 2) return launch_simt<2>(a, st);
-  if (a.G <= 4) return launch_simt<4>(a, st);
-  return launch_simt<8>(a, st);
+  switch (a.G) {
+    case 1: return launch_simt<1>(a, st);
+    case 2: return launch_simt<2>(a, st);
+    case 3: return launch_simt<3>(a, st);
+    case 4: return launch_simt<4>(a, st);
+    case 5: return launch_simt<5>(a, st);
+    case 6: return launch_simt<6>(a, st);
+    case 7: return launch_simt<7>(a, st);
+    default: return launch_simt<8>(a, st);
+  }
 }
 
 static size_t part_bytes(int D) {
   return ((size_t)2 * kPagedMaxCtas * kPagedHeads * (D + 1) * sizeof(float) + 255) & ~size_t(255);
 }
-size_t paged_decode_workspace_bytes(int D) { return part_bytes(D) + ((kPagedMaxCtas * sizeof(unsigned int) + 255) & ~size_t(255)); }
+size_t paged_decode_workspace_bytes(int D) {
+  return part_bytes(D) + ((kPagedMaxCtas * sizeof(unsigned int) + 255) & ~size_t(255));
+}
 void paged_decode_workspace_split(void* ws, int D, float** part, unsigned int** count) {
   *part = static_cast<float*>(ws);
   *count = reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(ws) + part_bytes(D));

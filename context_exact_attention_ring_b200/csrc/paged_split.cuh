@@ -292,7 +292,7 @@ struct PagedJoin {
   static constexpr bool BY_HEAD = G > 8;                        // groups over heads, not parts
   static constexpr int H = BY_HEAD ? 8 : G < 4 ? G : 4;         // heads at a time
   static constexpr int HL = BY_HEAD ? (H + NG - 1) / NG : H;    // heads of a lane
-  static constexpr int U = BY_HEAD ? 8 : 4;                     // parts a lane has in flight
+  static constexpr int U = BY_HEAD ? 8 : kThreads > 256 ? 1 : 4;    // parts a lane has in flight
   struct Smem {
     float w[kPagedMaxCtas * H];
     alignas(16) float4 o[BY_HEAD ? 1 : NG][BY_HEAD ? 1 : H][BY_HEAD ? 1 : D / 4];
