@@ -4,12 +4,14 @@
 //   need_b = ceil((len_b + new_b) / ps) - ceil(len_b / ps)
 // pages from the end of the free list, in order of sequence and page, and the
 // call's tokens, packed sequence after sequence, get their cache rows
-//   slot(t) = table[b][pos / ps] * ps + pos % ps,   pos = len_b + t - cu_b.
+//   slot(t) = page(pos / ps) * ps + pos % ps,   pos = len_b + t - cu_b.
 // Two prefix sums over the sequences (tokens, then pages, since whether a
-// sequence's tokens fit decides whether it takes pages) run in one block, which
-// also moves the pages.  The slots are one independent lookup each: a few
-// thousand are written by the same block, more by a second launch over the
-// whole GPU.
+// sequence's tokens fit decides whether it takes pages) run in one block,
+// which also moves the pages.  The slots are one independent lookup each: a few
+// thousand are written by the same block (a page not in the table before the
+// call is looked up in the free list, so nothing waits for the table), more by
+// a second launch over the whole GPU.  Latency-bound: a decode step moves a few
+// KB.
 //
 // page_trim shortens sequences and puts the pages past their new ends back,
 // last taken on top, so that extending and trimming by the same tokens leaves
@@ -22,12 +24,14 @@
 namespace ra {
 
 namespace pgt {
-constexpr int THREADS = 1024;
+constexpr int THREADS = 1024;             // of the block that scans; sequences of a chunk
 constexpr int NW = THREADS / 32;
-constexpr int ONE_LAUNCH_TOKENS = 4096;   // slots written by the first launch's block
+constexpr int ONE_LAUNCH_TOKENS = 4096;   // slots written by the first launch's block: 4 a thread
+constexpr int SLOT_THREADS = 256, SLOTS = 4;   // of the second launch: slots a thread
 }  // namespace pgt
 
 // Inclusive prefix sum over the block's threads; *total gets the sum of all.
+// Ends with every thread past its reads of s_warp.
 __device__ __forceinline__ long long block_scan(long long x, long long* s_warp, long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -37,130 +41,246 @@ __device__ __forceinline__ long long block_scan(long long x, long long* s_warp, 
   }
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    long long w = s_warp[lane];
+  long long w = s_warp[lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += up;
-    }
-    s_warp[lane] = w;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += up;
   }
+  const long long before = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+  *total = __shfl_sync(0xffffffffu, w, 31);
   __syncthreads();
-  if (warp > 0) x += s_warp[warp - 1];
-  *total = s_warp[pgt::NW - 1];
-  __syncthreads();
-  return x;
+  return warp ? x + before : x;
 }
 
 __device__ __forceinline__ int pages_of(long long len, int ps_log2) {
   return (int)((len + (1 << ps_log2) - 1) >> ps_log2);
 }
 
-// The slot of token t.
-__device__ __forceinline__ int slot_of(const ExtendArgs& a, int t) {
-  // last b with cu[b] <= t
-  int lo = 0, hi = a.B;
+// Last i in [lo, hi) with v[i] <= x (v ascending, v[lo] <= x).
+template <typename T>
+__device__ __forceinline__ int last_at_most(const T* v, int lo, int hi, T x) {
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (a.cu_new[mid] <= t) lo = mid; else hi = mid;
+    if (v[mid] <= x) lo = mid; else hi = mid;
   }
-  if (t >= a.cu_new[a.B]) return -1;
-  const int start = a.start_lens[lo];
-  if (start < 0) return -1;
-  const int pos = start + (t - a.cu_new[lo]);
-  const int page = a.table[(size_t)lo * a.table_stride + (pos >> a.ps_log2)];
-  if (page < 0 || page > (0x7fffffff >> a.ps_log2)) return -1;
-  return (page << a.ps_log2) | (pos & ((1 << a.ps_log2) - 1));
+  return lo;
 }
 
-__global__ void __launch_bounds__(pgt::THREADS, 1) page_extend_kernel(ExtendArgs a, int with_slots) {
+__device__ __forceinline__ int slot_at(int page, int pos, int ps_log2) {
+  if (page < 0 || page > (0x7fffffff >> ps_log2)) return -1;
+  return (page << ps_log2) | (pos & ((1 << ps_log2) - 1));
+}
+
+struct ScanSmem {
+  long long warp[pgt::NW];
+  long long off[pgt::THREADS];    // pages moved for the chunk's sequences before this one
+  int from[pgt::THREADS];         // first page of the table it concerns
+  int count[pgt::THREADS];        // pages moved
+  int cu[pgt::THREADS], start[pgt::THREADS];
+  int long_seq[pgt::THREADS], n_long;
+};
+
+// Moves pages j < s.count[i] of the chunk's n sequences: store(i, j, load(i, j)).
+// `total` pages are numbered through in s.off (those of a sequence that is not
+// served among them).  Up to four a thread, a thread finds its pages' sequences
+// by bisection.  More, a warp takes a sequence's first 128, four sequences'
+// first 32 in flight at once, and the block together the rest of the long ones.
+// (Extend and trim of 256 sequences with 40 pages: 7.5 us by bisection, 10 the
+// other way; of 1021 sequences with 33,000 pages: 65 and 36 us.)  Called by all
+// threads between barriers.
+template <typename Load, typename Store>
+__device__ __forceinline__ void move_pages(ScanSmem& s, int n, long long total, Load load, Store store) {
   using namespace pgt;
-  __shared__ long long s_warp[NW];
-  __shared__ int s_old[THREADS], s_need[THREADS];
-  __shared__ long long s_off[THREADS];
-  paged_begin();
+  constexpr int OWN = 128;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (total <= 4 * THREADS) {
+    for (long long g = tid; g < total; g += THREADS) {
+      const int i = last_at_most(s.off, 0, n, g), j = (int)(g - s.off[i]);
+      if (j < s.count[i]) store(i, j, load(i, j));
+    }
+    return;
+  }
+  if (tid < n && s.count[tid] > OWN) s.long_seq[atomicAdd(&s.n_long, 1)] = tid;
+  for (int i0 = warp; i0 < n; i0 += 4 * NW) {
+    int v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * NW;
+      v[u] = i < n && lane < s.count[i] ? load(i, lane) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * NW;
+      if (i < n && lane < s.count[i]) store(i, lane, v[u]);
+    }
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * NW;
+      if (i >= n || s.count[i] <= 32) continue;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) v[k] = lane + 32 * (k + 1) < s.count[i] ? load(i, lane + 32 * (k + 1)) : 0;
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (lane + 32 * (k + 1) < s.count[i]) store(i, lane + 32 * (k + 1), v[k]);
+    }
+  }
+  __syncthreads();
+  for (int q = 0; q < s.n_long; ++q) {
+    const int i = s.long_seq[q], m = s.count[i];
+    for (int j0 = OWN + tid; j0 < m; j0 += 4 * THREADS) {
+      int v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = j0 + u * THREADS < m ? load(i, j0 + u * THREADS) : 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (j0 + u * THREADS < m) store(i, j0 + u * THREADS, v[u]);
+    }
+  }
+}
+
+// One_launch: at most THREADS sequences and ONE_LAUNCH_TOKENS slots, written here.
+__global__ void __launch_bounds__(pgt::THREADS, 1) page_extend_kernel(ExtendArgs a, int one_launch) {
+  using namespace pgt;
+  __shared__ ScanSmem s;
+  paged_begin();
+  const int tid = threadIdx.x;
   const long long cap = (long long)a.W << a.ps_log2;
   const int n_free = min(max(*a.n_free, 0), a.max_free);
-  long long tokens = 0, pages = 0, taken = 0;   // of the sequences before this chunk
+  long long tokens = 0, pages = 0, taken = 0;   // of the sequences before this chunk; pages this call takes
   bool full = false;
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-    const int b = b0 + tid;
+    const int b = b0 + tid, in_chunk = min(THREADS, a.B - b0);
     const bool in = b < a.B;
     const long long len = in ? min(max((long long)a.seq_lens[b], 0LL), cap) : 0;
     const long long add = in ? max(a.new_lens[b], 0) : 0;
     long long total;
-    const long long cu1 = tokens + block_scan(add, s_warp, &total);
+    const long long cu1 = tokens + block_scan(add, s.warp, &total);
+    const long long cu0 = cu1 - add;
     tokens += total;
     const bool fits = in && len + add <= cap && cu1 <= a.max_tokens;
     const int old = pages_of(len, a.ps_log2);
     const int need = fits ? pages_of(len + add, a.ps_log2) - old : 0;
-    const long long upto = pages + block_scan(need, s_warp, &total);
-    pages += total;
-    const bool ok = fits && (need == 0 || upto <= n_free);
+    const long long upto = block_scan(need, s.warp, &total);
+    // the sequences served take the first pages of the list without a gap: once one finds too few,
+    // no later one that needs any is served
+    const bool ok = fits && (need == 0 || pages + upto <= n_free);
     full |= in && !ok;
-    const long long got = block_scan(ok ? need : 0, s_warp, &total);
-    (void)got;
-    taken += total;
     if (in) {
       if (b == 0) a.cu_new[0] = 0;
       a.cu_new[b + 1] = (int)min(cu1, 0x7fffffffLL);
       a.start_lens[b] = ok ? (int)len : -1;
       if (ok) a.seq_lens[b] = (int)(len + add);
     }
-    s_old[tid] = old;
-    s_need[tid] = ok ? need : 0;
-    s_off[tid] = upto - need;
+    s.off[tid] = upto - need;
+    s.from[tid] = old;
+    s.cu[tid] = (int)min(cu0, 0x7fffffffLL);
+    s.start[tid] = ok ? (int)len : -1;
+    s.count[tid] = ok ? need : 0;
+    if (tid == 0) s.n_long = 0;
+    const long long mine = ok && need ? pages + upto : 0;     // the last that this sequence takes
+    taken = max(taken, mine);
     __syncthreads();
-    // a warp per sequence moves its pages
-    for (int i = warp; i < THREADS && b0 + i < a.B; i += NW)
-      for (int j = lane; j < s_need[i]; j += 32)
-        a.table[(size_t)(b0 + i) * a.table_stride + s_old[i] + j] = a.free_pages[n_free - 1 - (s_off[i] + j)];
-    __syncthreads();
+    move_pages(s, in_chunk, total, [&](int i, int j) { return __ldg(a.free_pages + (n_free - 1 - (pages + s.off[i] + j))); },
+               [&](int i, int j, int page) { a.table[(size_t)(b0 + i) * a.table_stride + s.from[i] + j] = page; });
+    if (one_launch) {
+#pragma unroll 4
+      for (int t = tid; t < a.max_tokens; t += THREADS) {
+        int slot = -1;
+        if (t < tokens) {
+          const int i = last_at_most(s.cu, 0, in_chunk, t);
+          if (s.start[i] >= 0) {
+            const int pos = s.start[i] + (t - s.cu[i]), p = pos >> a.ps_log2;
+            const int page = p < s.from[i] ? a.table[(size_t)i * a.table_stride + p]
+                                           : a.free_pages[n_free - 1 - (s.off[i] + p - s.from[i])];
+            slot = slot_at(page, pos, a.ps_log2);
+          }
+        }
+        a.slot_map[t] = slot;
+      }
+    }
+    pages += total;
+    __syncthreads();    // s is free
   }
-  if (tid == 0) *a.n_free = n_free - (int)taken;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, o));
+  if ((tid & 31) == 0) s.warp[tid >> 5] = taken;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < NW; ++w) taken = max(taken, s.warp[w]);
+    *a.n_free = n_free - (int)taken;
+  }
   if (full) atomicCAS(a.err, 0u, kFaultCapacity);
-  if (with_slots)
-    for (int t = tid; t < a.max_tokens; t += THREADS) a.slot_map[t] = slot_of(a, t);
 }
 
-__global__ void __launch_bounds__(256) slot_map_kernel(ExtendArgs a) {
+// Slots [first, first + SLOT_THREADS * SLOTS) by each block: a warp finds the
+// sequence of the first and one that of the last (32 probes at once), the
+// threads bisect between them.
+__global__ void __launch_bounds__(pgt::SLOT_THREADS) slot_map_kernel(ExtendArgs a) {
+  using namespace pgt;
+  __shared__ int s_seq[2];
   paged_begin();
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t < a.max_tokens) a.slot_map[t] = slot_of(a, t);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int first = blockIdx.x * (SLOT_THREADS * SLOTS);
+  const int last = min(first + SLOT_THREADS * SLOTS, a.max_tokens) - 1;
+  const int all = a.cu_new[a.B];
+  if (warp < 2) {
+    const int t = min(warp ? last : first, max(all - 1, 0));
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const uint32_t le = __ballot_sync(0xffffffffu, at < hi && a.cu_new[min(at, a.B)] <= t);
+      lo += (__popc(le) - 1) * step;      // lane 0 always agrees
+      hi = min(hi, lo + step);
+    }
+    if (lane == 0) s_seq[warp] = lo;
+  }
+  __syncthreads();
+  const int lo = s_seq[0], hi = s_seq[1] + 1;
+#pragma unroll
+  for (int u = 0; u < SLOTS; ++u) {
+    const int t = first + u * SLOT_THREADS + threadIdx.x;
+    if (t > last) break;
+    int slot = -1;
+    if (t < all) {
+      const int b = last_at_most(a.cu_new, lo, hi, t);
+      const int start = a.start_lens[b];
+      if (start >= 0) {
+        const int pos = start + (t - a.cu_new[b]);
+        slot = slot_at(a.table[(size_t)b * a.table_stride + (pos >> a.ps_log2)], pos, a.ps_log2);
+      }
+    }
+    a.slot_map[t] = slot;
+  }
 }
 
 cudaError_t launch_page_extend(const ExtendArgs& a, cudaStream_t st) {
-  const int one = a.max_tokens <= pgt::ONE_LAUNCH_TOKENS;
+  const int one = a.max_tokens <= pgt::ONE_LAUNCH_TOKENS && a.B <= pgt::THREADS;
   const cudaError_t e = paged_launch(page_extend_kernel, 1, pgt::THREADS, 0, st, a, one);
   if (e != cudaSuccess || one) return e;
-  return paged_launch(slot_map_kernel, (a.max_tokens + 255) / 256, 256, 0, st, a);
+  constexpr int per = pgt::SLOT_THREADS * pgt::SLOTS;
+  return paged_launch(slot_map_kernel, (a.max_tokens - 1) / per + 1, pgt::SLOT_THREADS, 0, st, a);
 }
 
 __global__ void __launch_bounds__(pgt::THREADS, 1) page_trim_kernel(TrimArgs a) {
   using namespace pgt;
-  __shared__ long long s_warp[NW];
-  __shared__ int s_from[THREADS], s_gone[THREADS];
-  __shared__ long long s_off[THREADS];
+  __shared__ ScanSmem s;
   paged_begin();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x;
   const long long cap = (long long)a.W << a.ps_log2;
   const int n_free = min(max(*a.n_free, 0), a.max_free);
-  // pages given back by all sequences
-  long long all = 0;
-  for (int b = tid; b < a.B; b += THREADS) {
-    const long long len = min(max((long long)a.seq_lens[b], 0LL), cap);
-    const long long keep = min(max((long long)a.keep_lens[b], 0LL), len);
-    all += pages_of(len, a.ps_log2) - pages_of(keep, a.ps_log2);
+  long long all = 0, total;      // pages given back by all sequences
+  if (a.B > THREADS) {
+    for (int b = tid; b < a.B; b += THREADS) {
+      const long long len = min(max((long long)a.seq_lens[b], 0LL), cap);
+      const long long keep = min(max((long long)a.keep_lens[b], 0LL), len);
+      all += pages_of(len, a.ps_log2) - pages_of(keep, a.ps_log2);
+    }
+    block_scan(all, s.warp, &total);
+    all = total;
   }
-  long long total;
-  block_scan(all, s_warp, &total);
-  all = total;
-  const long long room = min(all, (long long)a.max_free - n_free);   // the list cannot hold more
   long long before = 0;
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-    const int b = b0 + tid;
+    const int b = b0 + tid, in_chunk = min(THREADS, a.B - b0);
     long long len = 0, keep = 0;
     if (b < a.B) {
       len = min(max((long long)a.seq_lens[b], 0LL), cap);
@@ -168,21 +288,25 @@ __global__ void __launch_bounds__(pgt::THREADS, 1) page_trim_kernel(TrimArgs a) 
     }
     const int from = pages_of(keep, a.ps_log2);
     const int gone = pages_of(len, a.ps_log2) - from;
-    const long long upto = before + block_scan(gone, s_warp, &total);
-    before += total;
-    s_from[tid] = from;
-    s_gone[tid] = gone;
-    s_off[tid] = upto - gone;
-    __syncthreads();
-    for (int i = warp; i < THREADS && b0 + i < a.B; i += NW)
-      for (int j = lane; j < s_gone[i]; j += 32) {
-        const long long to = n_free + all - 1 - (s_off[i] + j);
-        if (to < a.max_free) a.free_pages[to] = a.table[(size_t)(b0 + i) * a.table_stride + s_from[i] + j];
-      }
+    const long long upto = block_scan(gone, s.warp, &total);
+    if (a.B <= THREADS) all = total;
+    s.off[tid] = upto - gone;
+    s.from[tid] = from;
+    s.count[tid] = gone;
+    if (tid == 0) s.n_long = 0;
     if (b < a.B) a.seq_lens[b] = (int)keep;
     __syncthreads();
+    move_pages(s, in_chunk, total,
+               [&](int i, int j) { return __ldg(a.table + (size_t)(b0 + i) * a.table_stride + s.from[i] + j); },
+               [&](int i, int j, int page) {
+                 const long long to = n_free + all - 1 - (before + s.off[i] + j);
+                 if (to < a.max_free) a.free_pages[to] = page;     // the list cannot hold more
+               });
+    before += total;
+    __syncthreads();    // s is free
   }
   if (tid == 0) {
+    const long long room = min(all, (long long)a.max_free - n_free);
     *a.n_free = n_free + (int)room;
     if (room < all) atomicCAS(a.err, 0u, kFaultCapacity);
   }
