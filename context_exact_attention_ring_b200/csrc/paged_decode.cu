@@ -17,10 +17,11 @@
 //              dim t of O^T);
 //   warps 4, 6 producers of K (and Q) and of V: lane i owns page slot i of a
 //              tile (a tile holds 128 / page_size pages, or is part of one)
-//              and looks its page up one tile ahead; one lane then issues the
-//              pages' TMA boxes into a ring of 3 stages.  Issuing a box takes
-//              60-80 cycles, and a tile of 16-token pages is 32 boxes in the
-//              2700 cycles its bytes take: hence two warps.  The V producer
+//              and looks its page up one tile ahead; each lane issues its
+//              page's TMA boxes into a ring of 3 stages.  Issuing a box takes
+//              60-80 cycles (120 if one lane does it for all), and a tile of
+//              16-token pages is 32 boxes in the 2700 cycles its bytes take:
+//              hence two warps.  The V producer
 //              also leaves each slot's number of valid keys (its stage is
 //              not refilled before the softmax is done with the tile, as K's
 //              is);
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
     const uint64_t pol_kv = l2_policy_evict_first(), pol_q = l2_policy_evict_last();
     const int nslots = kPagedTile >> psn_log2;
-    PagedWalk walk(run, SEG_COST);
+    PagedWalk walk(a, rows, run, SEG_COST);
     PagedPiece pc;
     PagedHead hd{};
     int len = 0;
@@ -263,15 +264,11 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
       const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(sm.kv[s][is_k ? 0 : 1]);
       if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)__popc(live) * (uint32_t)(DH * 2) << psn_log2);
       __syncwarp();
-      for (uint32_t rest = live; rest; rest &= rest - 1) {
-        const int slot = __ffs(rest) - 1;
-        const int page = __shfl_sync(0xffffffffu, cur.page, slot), in_page = __shfl_sync(0xffffffffu, cur.in_page, slot);
-        const int c1 = maps.head_outer ? in_page : g, c2 = maps.head_outer ? g : in_page;
-        const uint32_t at = dst + ((uint32_t)slot << (psn_log2 + 7));
-        if (elect_one()) {
+      if (cur.valid > 0) {
+        const int c1 = maps.head_outer ? cur.in_page : g, c2 = maps.head_outer ? g : cur.in_page;
+        const uint32_t at = dst + ((uint32_t)lane << (psn_log2 + 7));
 #pragma unroll
-          for (int sl = 0; sl < DH / 64; ++sl) tma_load_4d(at + sl * SLAB, tmKV, fb, sl * 64, c1, c2, page, pol_kv);
-        }
+        for (int sl = 0; sl < DH / 64; ++sl) tma_load_4d(at + sl * SLAB, tmKV, fb, sl * 64, c1, c2, cur.page, pol_kv);
       }
       ++cnt;
     }
@@ -287,7 +284,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idS = paged_idesc(NQ, false), idPV = paged_idesc(NP, true);
-      PagedWalk walk(run, SEG_COST);
+      PagedWalk walk(a, rows, run, SEG_COST);
       PagedPiece pc;
       uint32_t t = 0, nu = 0;
       bool ok = true;
@@ -315,7 +312,11 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
         if (prev_last) mma_commit(smem_u32(&sm.o_full[ob]));
         return true;
       };
-      while (ok && walk.next(a, rows, pc)) {
+      PagedPiece nxt;
+      bool more = walk.next(a, rows, nxt);
+      while (ok && more) {
+        pc = nxt;
+        more = walk.next(a, rows, nxt);      // while the piece's first copies are on their way
         const int qb = nu & 1;
         if (!mbar_wait(smem_u32(&sm.q_full[qb]), (nu >> 1) & 1u, abort_flag, kWaitQFull, err)) { ok = false; break; }
         const uint64_t qdesc = sw128_desc(smem_u32(sm.q[qb]), 16, 1024);
@@ -423,11 +424,13 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
       return true;
     };
 
-    PagedWalk walk(run, SEG_COST);
+    PagedWalk walk(a, rows, run, SEG_COST);
     PagedPiece pc;
     uint32_t t = 0, nu = 0;
-    bool ok = true;
-    while (ok && walk.next(a, rows, pc)) {
+    PagedPiece nxt;
+    bool ok = true, more = walk.next(a, rows, nxt);
+    while (ok && more) {
+      pc = nxt;
       float m[G], l[G];      // per head: base (the same in every thread), this thread's sum
 #pragma unroll
       for (int h = 0; h < G; ++h) {
@@ -529,9 +532,12 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.p_full[sb]));
-        if (j == pc.a && nu > 0 && !finish()) {
-          ok = false;
-          break;
+        if (j == pc.a) {      // while the tile's products run
+          if (nu > 0 && !finish()) {
+            ok = false;
+            break;
+          }
+          more = walk.next(a, rows, nxt);
         }
       }
       if (!ok) break;

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
   // after the exchanges a lane holds key `mine` of its group's four
   const bool b1 = lr & (LPR / 2), b0 = lr & (LPR / 4);
   const int mine = (b1 ? 2 : 0) + (b0 ? 1 : 0);
-  PagedWalk walk(run, SEG_COST);
+  PagedWalk walk(a, rows, run, SEG_COST);
   PagedPiece pc;
   while (walk.next(a, rows, pc)) {
     const PagedHead hd = paged_head(a, pc.row, pc.sub, HEADS);

@@ -173,28 +173,38 @@ struct PagedPiece {
   int seg_t;       // first unit of the segment, counted over the call
 };
 struct PagedWalk {
-  int t, t1, row, row_t, seg_cost;
-  __device__ __forceinline__ PagedWalk(const PagedRun& r, int cost)
-      : t(r.t0), t1(r.t1), row(r.row), row_t(r.row_t), seg_cost(cost) {}
+  int t1, seg_cost;
+  int row, sub, nt, nu, seg_t, from;    // the next segment: its tiles, units, first unit; the unit of it to begin at
+  __device__ __forceinline__ PagedWalk(const PagedDecodeArgs& a, const PagedRows& rows, const PagedRun& r, int cost)
+      : t1(r.t1), seg_cost(cost), row(r.row), sub(0), nt(0), nu(0), seg_t(r.row_t), from(0) {
+    if (r.t0 >= t1) {
+      seg_t = t1;
+      return;
+    }
+    nt = paged_tiles(a, row);
+    nu = paged_units(nt, seg_cost);
+    from = r.t0 - seg_t;
+    sub = from / nu;
+    seg_t += sub * nu;
+    from -= sub * nu;
+  }
   __device__ __forceinline__ bool next(const PagedDecodeArgs& a, const PagedRows& rows, PagedPiece& p) {
-    while (t < t1) {
-      int nt = paged_tiles(a, row), nu = paged_units(nt, seg_cost);
-      while (t - row_t >= nu * rows.mult) {    // never past the last row: t < t1 <= T
-        row_t += nu * rows.mult;
-        ++row;
-        nt = paged_tiles(a, row);
+    while (seg_t < t1) {
+      const bool whole = nt <= kPagedWhole;
+      p.row = row;
+      p.sub = sub;
+      p.nt = nt;
+      p.seg_t = seg_t;
+      p.a = from;
+      p.b = whole ? (from > 0 ? 0 : nt) : min(nt, t1 - seg_t);
+      from = 0;
+      seg_t += nu;
+      if (seg_t < t1 && ++sub == rows.mult) {      // a row with keys follows: t1 <= T
+        sub = 0;
+        do nt = paged_tiles(a, ++row);
+        while (nt == 0);
         nu = paged_units(nt, seg_cost);
       }
-      const int o = t - row_t;
-      p.row = row;
-      p.sub = o / nu;
-      p.nt = nt;
-      p.a = o - p.sub * nu;
-      const bool whole = nt <= kPagedWhole;
-      const int end = whole ? nu : min(nu, p.a + (t1 - t));
-      p.b = whole && p.a > 0 ? 0 : min(nt, end);
-      p.seg_t = row_t + p.sub * nu;
-      t += end - p.a;
       if (p.a < p.b) return true;    // else the tail of a segment, or the rest of one that is not split
     }
     return false;
