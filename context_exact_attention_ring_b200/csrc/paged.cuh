@@ -5,14 +5,13 @@
 
 namespace ra {
 
-// All threads, before the first access to global memory: lets the next kernel
-// of the stream start early, and waits until the one before has completed.
-// No thread skips the wait, so a kernel's completion implies that of all
-// kernels before it on the stream.
-__device__ __forceinline__ void paged_begin() {
-  grid_launch_dependents();
-  grid_dependency_wait();
-}
+// All threads, before the first access to global memory: waits until the
+// kernel before it on the stream has completed.  No thread skips the wait, so a
+// kernel's completion implies that of all kernels before it.  The next kernel
+// is not invited in early (griddepcontrol.launch_dependents): a ring step may
+// follow, which reads its shards and blocks without waiting, and these may be
+// what the kernel here writes.  It starts as this one's CTAs exit.
+__device__ __forceinline__ void paged_begin() { grid_dependency_wait(); }
 
 // Maximum over the warp's lanes (NaN ignored, as fmaxf does).
 __device__ __forceinline__ float warp_max_redux(float v) {

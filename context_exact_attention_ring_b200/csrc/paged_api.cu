@@ -153,10 +153,10 @@ ring_status ring_attn_decode_paged(const void* q, const void* k_pool, const void
   const int eb = elem_bytes(dtype);
   if (!good_rows(q_stride_b, q_stride_h, B, Hq, D, eb)) return RING_EINVAL;
   if (!table_fits(W, pl) || table_stride >= (size_t(1) << 32) || (sel && !table_fits(K, pl))) return RING_EINVAL;
-  // tiles of the call are counted in 32 bits (a segment is a kv head's group of at most 16 query heads, or 8)
+  // units of the call (tiles, and one per segment: a kv head's group of at most 8 query heads or more) count in 32 bits
   const long long keys = (long long)(sel ? K : W) << pl;
   const long long segs = (long long)B * Hkv * ((Hq / Hkv + 7) / 8);
-  if (segs * ((keys + kPagedTile - 1) / kPagedTile) > 0x7fffffffLL || (long long)B * Hq * D > 0x7fffffffLL)
+  if (segs * ((keys + kPagedTile - 1) / kPagedTile + 1) > 0x7fffffffLL || (long long)B * Hq * D > 0x7fffffffLL)
     return RING_EINVAL;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < paged_decode_workspace_bytes(D))
     return RING_EINVAL;
