@@ -94,6 +94,26 @@ def test_extend_and_trim_many_sequences_and_shortage(B, max_tokens, room):
     assert sl.tolist() == ref.lens and nf.tolist() == [ref.n] and fr.tolist() == ref.free
 
 
+def test_extend_and_trim_long_sequences():
+    # sequences of several hundred pages, moved by the whole block; a free list that is full again
+    need_cuda()
+    ps, W = 8, 4000
+    lens, news = [5, 16000, 0, 77, 1], [9000, 1, 20000, 0, 6400]
+    table, free = _tables(lens, ps, W, 4600, 9)
+    ref = R.Tables(lens, table, free, len(free), ps)
+    sl, tb, fr, nf = ints(lens), ints(table), ints(free), ints([len(free)])
+    slots, start, cu = ra.ring_attn_page_extend(sl, ints(news), tb, fr, nf, ps, max_tokens=sum(news) + 3)
+    w_slots, w_start, w_cu, short = ref.extend(news, sum(news) + 3)
+    ok()
+    assert not short and slots.tolist() == w_slots and start.tolist() == w_start and cu.tolist() == w_cu
+    assert np.array_equal(tb.cpu().numpy(), ref.table) and nf.tolist() == [ref.n]
+    keep = [0, 16001, 0, 0, 100]
+    ref.trim(keep)
+    ra.ring_attn_page_trim(sl, ints(keep), tb, fr, nf, ps)
+    ok()
+    assert sl.tolist() == ref.lens and nf.tolist() == [ref.n] and fr.tolist() == ref.free
+
+
 # ---------------------------------------------------------------- append
 def make_pools(layout, N, ps, Hkv, D, dtype, fill=None):
     """k, v pools [N, ps, Hkv, D] in the memory layout named."""
@@ -106,16 +126,18 @@ def make_pools(layout, N, ps, Hkv, D, dtype, fill=None):
         k, v = both[:, 0], both[:, 1]
     elif layout == "heads_first":      # pages of [Hkv, ps, D]
         k, v = (new(N, Hkv, ps, D).transpose(1, 2) for _ in range(2))
-    else:                              # K and V of a token next to each other
+    elif layout == "kv_token":         # K and V of a token next to each other
         both = new(N, ps, 2, Hkv, D)
         k, v = both[:, :, 0], both[:, :, 1]
+    else:                              # the tokens of a page far apart
+        k, v = (new(ps, N, Hkv, D).transpose(0, 1) for _ in range(2))
     if fill is not None:
         k.copy_(fill[0])
         v.copy_(fill[1])
     return k, v
 
 
-LAYOUTS = ["plain", "kv_page", "heads_first", "kv_token"]
+LAYOUTS = ["plain", "kv_page", "heads_first", "kv_token", "tokens_apart"]
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
@@ -377,3 +399,212 @@ def test_select(W, K, first, last):
     w_sel, w_n = R.select(sc, lens, ps, K, first, last)
     assert np.array_equal(n.cpu().numpy(), w_n)
     assert np.array_equal(sel.cpu().numpy(), w_sel)
+
+
+# ---------------------------------------------------------------- addresses, streams, graphs
+def test_offsets_beyond_32_bits():
+    # pools of 2.2e9 elements (4.4 GB each); the tokens lie in the last pages and in the first
+    need_cuda()
+    ps, Hkv, D = 64, 4, 128
+    N = 2 ** 31 // (ps * Hkv * D) + 3000
+    k = torch.empty((N, ps, Hkv, D), device="cuda", dtype=torch.bfloat16)
+    v = torch.empty_like(k)
+    n = 5 * ps - 7
+    pages = [N - 1, 0, N - 2, 3, N - 3]
+    tb = ints([pages])
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kn = torch.randn((n, Hkv, D), generator=g, device="cuda").to(torch.bfloat16)
+    vn = torch.randn((n, Hkv, D), generator=g, device="cuda").to(torch.bfloat16)
+    slots = ints([pages[t // ps] * ps + t % ps for t in range(n)])
+    ra.ring_attn_paged_append(k, v, kn, vn, slots)
+    q = queries(1, 8, D, "bf16", 4)
+    out, lse = ra.ring_attn_decode_paged(q, k, v, tb, ints([n]))
+    bnd = ra.ring_attn_page_bounds(k, tb, ints([n]))
+    sc = ra.ring_attn_page_scores(q, bnd, tb, ints([n]), ps)
+    ok()
+    # the same tokens in a pool of five pages
+    small = [(x.new_zeros((5, ps, Hkv, D))) for x in (k, v)]
+    for x, new in zip(small, (kn, vn)):
+        x.view(-1, Hkv, D)[:n] = new
+        x.view(-1, Hkv, D)[n:] = float("nan")
+    stb = ints([[0, 1, 2, 3, 4]])
+    out2, lse2 = ra.ring_attn_decode_paged(q, *small, stb, ints([n]))
+    bnd2 = ra.ring_attn_page_bounds(small[0], stb, ints([n]))
+    sc2 = ra.ring_attn_page_scores(q, bnd2, stb, ints([n]), ps)
+    ok()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2) and torch.equal(bnd[pages], bnd2) and torch.equal(sc, sc2)
+    check_decode(out2, lse2, R.decode(q, *small, stb, [n], 1 / math.sqrt(D)), D)
+
+
+def test_two_streams_with_a_workspace_each():
+    need_cuda()
+    cases = []
+    for seed, lens in ((51, [3000, 20, 777, 6000]), (52, [100, 9000, 0, 5])):
+        k, v, tb = make_cache(lens, 16, 2, 128, "bf16", seed)
+        q = queries(4, 8, 128, "bf16", seed)
+        cases.append((q, k, v, tb, ints(lens), ra.decode_paged_workspace(128), torch.cuda.Stream()))
+    want = [ra.ring_attn_decode_paged(*c[:5], workspace=c[5]) for c in cases]
+    ok()
+    got = []
+    for _ in range(20):
+        for c in cases:
+            c[6].wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(c[6]):
+                got.append(ra.ring_attn_decode_paged(*c[:5], workspace=c[5]))
+    ok()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+
+
+def test_two_graphs_that_share_a_workspace_follow_the_lengths():
+    # captured calls read lengths, tables and lists on the device; replayed in turn on one stream
+    need_cuda()
+    k, v, tb = make_cache([4000] * 3, 16, 2, 64, "bf16", 61, garbage=False)
+    q = queries(3, 16, 64, "bf16", 62)
+    sl = ints([10, 2000, 4000])
+    sel = ints([[[0, 3, 9, 200], [1, 2, 100, 249]]] * 3)
+    n_sel = ints([[4, 3]] * 3)
+    ws = ra.decode_paged_workspace(64)
+    outs = [(torch.empty((3, 16, 64), device="cuda", dtype=torch.bfloat16), torch.empty((3, 16), device="cuda"))
+            for _ in range(2)]
+
+    def dense():
+        ra.ring_attn_decode_paged(q, k, v, tb, sl, out=outs[0][0], out_lse=outs[0][1], workspace=ws)
+
+    def sparse():
+        ra.ring_attn_decode_paged(q, k, v, tb, sl, sel=sel, n_sel=n_sel, out=outs[1][0], out_lse=outs[1][1], workspace=ws)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        dense()
+        sparse()
+    torch.cuda.synchronize()
+    graphs = []
+    for f in (dense, sparse):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            f()
+        graphs.append(gr)
+    for lens, ns in (([10, 2000, 4000], 4), ([0, 1, 3999], 2), ([4000, 129, 128], 3)):
+        sl.copy_(ints(lens))
+        n_sel.fill_(ns)
+        for gr in graphs:
+            gr.replay()
+        ok()
+        check_decode(*outs[0], R.decode(q, k, v, tb, lens, 1 / 8), 64)
+        check_decode(*outs[1], R.decode(q, k, v, tb, lens, 1 / 8, sel.cpu(), n_sel.cpu()), 64)
+
+
+# ---------------------------------------------------------------- the operators together
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,ps", [("bf16", 8, 2, 128, 16), ("fp32", 4, 1, 64, 32)])
+def test_serving_loop(dtype, Hq, Hkv, D, ps):
+    """Prompts of different lengths are admitted and decoded step by step through
+    a paged cache; one request ends, its pages go to a new one; every step's
+    attention (all pages, and the selected ones) is compared with 64-bit
+    attention over the request's own keys, and the whole step is replayed from
+    a graph."""
+    need_cuda()
+    dt, B, W, N = DT[dtype], 4, 40, 60
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    k_pool, v_pool = make_pools("kv_page", N, ps, Hkv, D, dt)
+    k_pool.fill_(float("nan"))                       # rows that no token was written to
+    v_pool.fill_(float("nan"))
+    bounds = torch.full((N, Hkv, 2, D), float("nan"), device="cuda", dtype=dt)
+    table = torch.full((B, W), -1, device="cuda", dtype=torch.int32)
+    free = torch.arange(N, device="cuda", dtype=torch.int32)
+    n_free, lens = ints([N]), ints([0] * B)
+    ws = ra.decode_paged_workspace(D)
+    keys = [[] for _ in range(B)]                    # the tokens each request has, on the host
+    K = 4
+
+    def admit(news):
+        T = sum(news)
+        kv = torch.randn((T, 2 * Hkv, D), generator=gen, device="cuda").to(dt)
+        slots, start, cu = ra.ring_attn_page_extend(lens, ints(news), table, free, n_free, ps, max_tokens=T)
+        ra.ring_attn_paged_append(k_pool, v_pool, kv[:, :Hkv], kv[:, Hkv:], slots)
+        ra.ring_attn_page_bounds(k_pool, table, lens, bounds=bounds, start_lens=start)
+        at = 0
+        for b, n in enumerate(news):
+            keys[b].append(kv[at:at + n].double().cpu())
+            at += n
+
+    # one step's buffers: a graph replays on them
+    qkv = torch.zeros((B, Hq + 2 * Hkv, D), device="cuda", dtype=dt)
+    one, order = ints([1, 1, 0, 1]), ints([0, 1, 3, 3])
+    slots, start, cu = torch.empty(B, device="cuda", dtype=torch.int32), torch.empty(B, device="cuda", dtype=torch.int32), \
+        torch.empty(B + 1, device="cuda", dtype=torch.int32)
+    outs = [(torch.empty((B, Hq, D), device="cuda", dtype=dt), torch.empty((B, Hq), device="cuda")) for _ in range(2)]
+    scores = torch.empty((B, Hkv, W), device="cuda")
+    sel, n_sel = torch.empty((B, Hkv, K), device="cuda", dtype=torch.int32), torch.empty((B, Hkv), device="cuda", dtype=torch.int32)
+
+    def step():
+        q, kn, vn = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        ra.ring_attn_page_extend(lens, one, table, free, n_free, ps, slot_map=slots, start_lens=start, cu_new=cu)
+        # the tokens, packed; the slot past them is -1
+        ra.ring_attn_paged_append(k_pool, v_pool, kn.index_select(0, order), vn.index_select(0, order), slots)
+        ra.ring_attn_page_bounds(k_pool, table, lens, bounds=bounds, start_lens=start)
+        ra.ring_attn_decode_paged(q, k_pool, v_pool, table, lens, out=outs[0][0], out_lse=outs[0][1], workspace=ws)
+        ra.ring_attn_page_scores(q, bounds, table, lens, ps, scores=scores)
+        ra.ring_attn_page_select(scores, lens, ps, K, keep_first=1, keep_last=1, sel=sel, n_sel=n_sel)
+        ra.ring_attn_decode_paged(q, k_pool, v_pool, table, lens, sel=sel, n_sel=n_sel, out=outs[1][0],
+                                  out_lse=outs[1][1], workspace=ws)
+
+    def check():
+        n = [sum(x.shape[0] for x in r) for r in keys]
+        assert lens.tolist() == n
+        # what the references gather through the table is the tokens themselves
+        tbl = table.cpu().numpy()
+        for b in range(B):
+            own = torch.cat(keys[b]) if keys[b] else torch.zeros((0, 2 * Hkv, D), dtype=torch.float64)
+            assert torch.equal(R.keys_of(k_pool.cpu(), tbl[b], n[b], ps), own[:, :Hkv])
+            assert torch.equal(R.keys_of(v_pool.cpu(), tbl[b], n[b], ps), own[:, Hkv:])
+        q = qkv[:, :Hq]
+        check_decode(*outs[0], R.decode(q, k_pool, v_pool, table, n, 1 / math.sqrt(D)), D)
+        check_decode(*outs[1], R.decode(q, k_pool, v_pool, table, n, 1 / math.sqrt(D), sel.cpu(), n_sel.cpu()), D)
+        w_sel, w_n = R.select(scores, n, ps, K, 1, 1)
+        assert np.array_equal(sel.cpu().numpy(), w_sel) and np.array_equal(n_sel.cpu().numpy(), w_n)
+        ref, mag = R.scores(q, bounds, table, n, ps)
+        none = torch.isneginf(ref)
+        assert torch.equal(torch.isneginf(scores.cpu()), none)
+        assert ((scores.cpu().double() - ref)[~none].abs() <= 2 * D * 2.0 ** -24 * mag[~none] + 1e-30).all()
+
+    def feed():
+        new = torch.randn(qkv.shape, generator=gen, device="cuda").to(dt)
+        qkv.copy_(new)
+        for b in (0, 1, 3):
+            keys[b].append(new[b:b + 1, Hq:].double().cpu())
+
+    admit([5 * ps + 3, ps - 1, 0, 12 * ps])
+    feed()
+    step()                                             # eager
+    ok()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(ps + 2):                            # over a page's end
+        feed()
+        graph.replay()
+        if i in (0, 1, ps, ps + 1):
+            ok()
+            check()
+    ok()
+    # request 3 ends; its pages serve a new prompt, and request 1 is rolled back by 3 tokens
+    before = int(n_free)
+    keep = lens.clone()
+    keep[3] = 0
+    keep[1] -= 3
+    ra.ring_attn_page_trim(lens, keep, table, free, n_free, ps)
+    assert int(n_free) > before + 12
+    keys[3] = []
+    flat = torch.cat(keys[1])
+    keys[1] = [flat[:-3]]
+    admit([0, 2, 0, 20 * ps + 1])
+    feed()
+    graph.replay()
+    ok()
+    check()
+    # pages in use and pages free are all pages, once each
+    n = lens.tolist()
+    used = [int(table[b, i]) for b in range(B) for i in range(R.cdiv(n[b], ps))]
+    assert sorted(used + free[:int(n_free)].tolist()) == list(range(N))
