@@ -120,15 +120,15 @@ cudaError_t launch_page_bounds(const BoundsArgs& a, cudaStream_t st) {
 
 // ---------------------------------------------------------------------------
 // scores.  Bound by the bytes of the bounds.  A half-warp shares a page, 8 (or
-// 4) dims a lane in 16-byte pieces, and holds four pages at once; the group's
+// 4) dims a lane in 16-byte pieces, and holds two pages at once; the group's
 // queries wait in shared memory, so that any number of heads takes one pass.
 // max(q lo, q hi) is q times hi or lo by the sign of q: a select and an FMA.
-// The four pages' sums are added up across the half-warp by halving: after two
-// exchanges a lane has one page, in six shuffles instead of sixteen.
+// The two pages' sums are added up across the half-warp by halving: after one
+// exchange a lane has one page.
 // ---------------------------------------------------------------------------
 namespace pgsc {
 constexpr int THREADS = 256;
-constexpr int U = 4;                              // pages of a half-warp
+constexpr int U = 2;                              // pages of a half-warp
 constexpr int PPB = THREADS / 16 * U;             // pages of a block at a time
 }  // namespace pgsc
 
@@ -168,7 +168,7 @@ __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(pgsc::THREADS) page_scores_kernel(ScoresArgs a, int G) {
+__global__ void __launch_bounds__(pgsc::THREADS, 4) page_scores_kernel(ScoresArgs a, int G) {
   using namespace pgsc;
   using Row = Sixteenth<T, D>;
   constexpr int N = Row::N;
@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(pgsc::THREADS) page_scores_kernel(ScoresArgs a
   }
   __syncthreads();
   const int lane = threadIdx.x & 31, l = lane & 15;
-  const bool b1 = l & 8, b0 = l & 4;
-  const int mine = (b1 ? 2 : 0) + (b0 ? 1 : 0);
+  const bool b0 = l & 8;
+  const int mine = b0 ? 1 : 0;
   float* out = a.scores + (size_t)blockIdx.y * a.W;
   const int32_t* table = a.table + (size_t)b * a.table_stride;
   for (int p0 = blockIdx.x * PPB; p0 < a.W; p0 += gridDim.x * PPB) {
@@ -220,20 +220,17 @@ __global__ void __launch_bounds__(pgsc::THREADS) page_scores_kernel(ScoresArgs a
 #pragma unroll
           for (int i = 0; i < N; ++i) s[u] = fmaf(qd[i], qd[i] < 0.f ? lo[u][i] : hi[u][i], s[u]);
         }
-        // keep two pages and send the others' sums, then one
-        float s0 = b1 ? s[2] : s[0], s1 = b1 ? s[3] : s[1];
-        s0 += __shfl_xor_sync(0xffffffffu, b1 ? s[0] : s[2], 8);
-        s1 += __shfl_xor_sync(0xffffffffu, b1 ? s[1] : s[3], 8);
-        float x = b0 ? s1 : s0;
-        x += __shfl_xor_sync(0xffffffffu, b0 ? s0 : s1, 4);
+        // keep one page and send the other's sum
+        float x = (b0 ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, b0 ? s[0] : s[1], 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         nan |= x != x;
         best = fmaxf(best, x);
       }
       if (nan) best = CUDART_NAN_F;
-      if ((l & 3) == 0 && first + mine < a.W) out[first + mine] = live >> mine & 1 ? best : -CUDART_INF_F;
-    } else if ((l & 3) == 0 && first + mine < a.W) {
+      if ((l & 7) == 0 && first + mine < a.W) out[first + mine] = live >> mine & 1 ? best : -CUDART_INF_F;
+    } else if ((l & 7) == 0 && first + mine < a.W) {
       out[first + mine] = -CUDART_INF_F;
     }
   }
