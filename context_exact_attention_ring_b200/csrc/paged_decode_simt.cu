@@ -4,13 +4,17 @@
 // in one pass over the keys with a running maximum and sum.  The tensor cores
 // have no float32 product; every product and sum here is float32.
 //
-// A CTA of 16 warps takes the tiles of its run (paged_split.cuh), 8 keys a
-// warp.  D / 4 lanes share a key row (one contiguous load), and each lane keeps
-// 4 dims of the outputs of up to 8 heads in registers, as packed pairs.  Four keys go through at once: their partial scores are added up
-// across the lanes by halving (2 + 1 exchanges leave a lane one key, the rest
-// are plain), so that a lane ends with one score and takes one exponential per
-// head, and the four weights return by shuffles.  Bound by memory for few heads and
-// by instructions for many: about 55 per head and four keys of a warp.
+// A CTA of 16 warps takes the tiles of its run (paged_split.cuh) in units of 8
+// keys to a group of D / 4 lanes, which share a key row (one contiguous load);
+// a lane keeps 4 dims of the outputs of up to 8 heads in registers, as packed
+// pairs.  K and V come by asynchronous copies into slots that the copying lane
+// itself reads, so that no barrier is needed: the next unit's K while this
+// one's V is used, its V during the next scores.  The 8 partial scores of a head
+// are added up across the lanes by halving (4 + 2 + 1 exchanges leave a lane one
+// key), so that a lane takes one maximum and one exponential per head; the
+// weights return through shared memory as pairs.  Bound by instructions, about
+// 85 per head and 8 keys of a group, above two heads, and by memory below.
+// (Four keys at a time: 62 us for 400,000 rows of 5 heads of 64, eight: 57.)
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -22,11 +26,9 @@ namespace ra {
 namespace pds {
 constexpr int THREADS = 512;
 constexpr int NW = THREADS / 32;
-constexpr int KPW = kPagedTile / NW;   // keys of a tile a warp takes
 constexpr int HEADS = 8;               // query heads of a group, at most
 constexpr int SEG_COST = 1;            // what a segment costs besides its tiles, in tiles
 constexpr int PARTS_PER_TILE = 10;     // parts joined in the time of a tile
-static_assert(KPW == 8, "a warp's keys lie in one page (pages hold at least 8 tokens)");
 }  // namespace pds
 
 template <int G, int D>
@@ -35,17 +37,26 @@ struct SimtSmem {
   alignas(16) float q[G][D];
   float m[pds::NW][G], l[pds::NW][G];
   int last;
+  // (weight, weight) per key of a lane group and head
+  alignas(16) float2 p[pds::NW][128 / D][8][(G + 1) & ~1];
   union {
-    float o[pds::NW][G][D];
+    uint4 kv[2][8][pds::THREADS];                         // K and V: 16 bytes of 8 keys for every lane
+    float o[pds::NW][G][D];                               // between pieces
     typename PagedJoin<pds::THREADS, G, D>::Smem join;
   };
 };
 
+// 16 bytes to shared memory in the background; zeros (and no read) where !ok.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0)
+               : "memory");
+}
+
 template <int G, int D>
 __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(PagedDecodeArgs a) {
   using namespace pds;
-  constexpr int LPR = D / 4, RPW = 32 / LPR;      // lanes of a row, rows a warp loads at once
-  constexpr int NB = KPW / (4 * RPW);             // batches of 4 keys per group of lanes
+  constexpr int LPR = D / 4, RPW = 32 / LPR;      // lanes of a row, groups of a warp
+  constexpr int UNIT = 8 * RPW;                   // keys a warp takes at a time, 8 a group (pages hold at least 8)
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SimtSmem<G, D>& sm = *reinterpret_cast<SimtSmem<G, D>*>(smem_raw);
   paged_begin();
@@ -54,9 +65,9 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
   const PagedRun run = paged_run<THREADS>(a, sm.run, paged_first_tiles(a), SEG_COST, PARTS_PER_TILE);
   paged_empty_rows(a, tid, THREADS);
   const float sl2 = a.scale * 1.4426950408889634f;
-  // after the exchanges a lane holds key `mine` of its group's four
-  const bool b1 = lr & (LPR / 2), b0 = lr & (LPR / 4);
-  const int mine = (b1 ? 2 : 0) + (b0 ? 1 : 0);
+  // after the exchanges a lane holds key `mine` of its group's eight
+  const bool b2 = lr & (LPR / 2), b1 = lr & (LPR / 4), b0 = lr & (LPR / 8);
+  const int mine = (b2 ? 4 : 0) + (b1 ? 2 : 0) + (b0 ? 1 : 0);
   PagedWalk walk(a, rows, run, SEG_COST);
   PagedPiece pc;
   while (walk.next(a, rows, pc)) {
@@ -78,67 +89,104 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
       l[h] = 0.f;
     }
     __syncthreads();
-    auto span = [&](int t) { return paged_span(a, hd.b, hd.g, len, t * kPagedTile + warp * KPW, KPW); };
-    PagedSpan next = span(pc.a);
-    for (int t = pc.a; t < pc.b; ++t) {
-      PagedSpan sp = next;
-      if (t + 1 < pc.b) next = span(t + 1);
-      sp.valid = paged_valid(a, sp);
-      if (sp.valid == 0) continue;                // the same in the whole warp
-      const size_t base = (size_t)sp.page * a.pool.page + (size_t)sp.in_page * a.pool.token +
+    const int nunits = (pc.b - pc.a) * (kPagedTile / UNIT);
+    auto span = [&](int i) { return paged_span(a, hd.b, hd.g, len, pc.a * kPagedTile + i * UNIT + grp * 8, 8); };
+    // 16 bytes of 8 keys of K (which 0) or V (1) to this lane's slots
+    auto copy = [&](const PagedSpan& sp, int which) {
+      const size_t base = (size_t)(sp.valid ? sp.page : 0) * a.pool.page + (size_t)sp.in_page * a.pool.token +
                           (size_t)hd.g * a.pool.head + 4 * lr;
-      const float* kr = static_cast<const float*>(a.k) + base;
-      const float* vr = static_cast<const float*>(a.v) + base;
-#pragma unroll 1
-      for (int n = 0; n < NB; ++n) {
-        ulonglong2 kx[4], vx[4];
+      const float* row = static_cast<const float*>(which ? a.v : a.k) + base;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int key = (n * 4 + u) * RPW + grp;
-          kx[u] = vx[u] = make_ulonglong2(0ull, 0ull);
-          if (key < sp.valid) {
-            kx[u] = __ldg(reinterpret_cast<const ulonglong2*>(kr + (size_t)key * a.pool.token));
-            vx[u] = __ldg(reinterpret_cast<const ulonglong2*>(vr + (size_t)key * a.pool.token));
-          }
-        }
-        const bool valid = (n * 4 + mine) * RPW + grp < sp.valid;
+      for (int u = 0; u < 8; ++u) {
+        const bool ok = u < sp.valid;
+        copy16(&sm.kv[which][u][tid], row, ok);
+        if (ok) row += a.pool.token;
+      }
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    PagedSpan cur, next;
+    cur.valid = next.valid = 0;
+    cur.page = next.page = cur.in_page = next.in_page = 0;
+    if (warp < nunits) {
+      cur = span(warp);
+      cur.valid = paged_valid(a, cur);
+      copy(cur, 0);
+      commit();
+      copy(cur, 1);
+    }
+    commit();
+    if (warp + NW < nunits) next = span(warp + NW);
+    for (int i = warp; i < nunits; i += NW) {
+      const bool more = i + NW < nunits;
+      next.valid = more ? paged_valid(a, next) : 0;
+      asm volatile("cp.async.wait_group 1;" ::: "memory");      // K of this unit
+      const bool valid = mine < cur.valid;
+      {
+        ulonglong2 kx[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) kx[u] = *reinterpret_cast<const ulonglong2*>(&sm.kv[0][u][tid]);
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&sm.q[h][4 * lr]);
-          float s[4];
+          float s[8];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) s[u] = hsum2(ffma2(q.x, kx[u].x, fmul2(q.y, kx[u].y)));
-          // keep two keys and send the others' sums, then one
-          float s0 = b1 ? s[2] : s[0], s1 = b1 ? s[3] : s[1];
-          s0 += __shfl_xor_sync(0xffffffffu, b1 ? s[0] : s[2], LPR / 2);
-          s1 += __shfl_xor_sync(0xffffffffu, b1 ? s[1] : s[3], LPR / 2);
-          float x = b0 ? s1 : s0;
-          x += __shfl_xor_sync(0xffffffffu, b0 ? s0 : s1, LPR / 4);
+          for (int u = 0; u < 8; ++u) s[u] = hsum2(ffma2(q.x, kx[u].x, fmul2(q.y, kx[u].y)));
+          // keep half of the keys and send the sums of the others, three times
 #pragma unroll
-          for (int o = LPR / 8; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+          for (int u = 0; u < 4; ++u) {
+            const float keep = b2 ? s[4 + u] : s[u], send = b2 ? s[u] : s[4 + u];
+            s[u] = keep + __shfl_xor_sync(0xffffffffu, send, LPR / 2);
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float keep = b1 ? s[2 + u] : s[u], send = b1 ? s[u] : s[2 + u];
+            s[u] = keep + __shfl_xor_sync(0xffffffffu, send, LPR / 4);
+          }
+          float x = (b0 ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, b0 ? s[0] : s[1], LPR / 8);
+#pragma unroll
+          for (int o = LPR / 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
           if (!valid) x = -CUDART_INF_F;
           const float mx = warp_max_redux(x);
-          if (mx > m[h]) {                        // the same in the whole warp
-            const float alpha = exp2f(m[h] - mx);
+          if (mx > m[h]) {                          // the same in the whole warp
+            const float alpha = ex2(m[h] - mx);
             const uint64_t al2 = pack2(alpha, alpha);
             l[h] *= alpha;
             acc[h][0] = fmul2(acc[h][0], al2);
             acc[h][1] = fmul2(acc[h][1], al2);
             m[h] = mx;
           }
-          const float p = x == -CUDART_INF_F ? 0.f : exp2f(x - m[h]);
-          l[h] += p;                              // every key in LPR / 4 lanes
+          const float p = x == -CUDART_INF_F ? 0.f : ex2(x - m[h]);
+          l[h] += p;                                // every key in LPR / 8 lanes
+          if (lr % (LPR / 8) == 0) sm.p[warp][grp][mine][h] = make_float2(p, p);
+        }
+      }
+      if (more) copy(next, 0);
+      commit();
+      asm volatile("cp.async.wait_group 1;" ::: "memory");      // V of this unit
+      __syncwarp();
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int src = grp * LPR + (u & 2 ? LPR / 2 : 0) + (u & 1 ? LPR / 4 : 0);
-            const float pu = __shfl_sync(0xffffffffu, p, src);
-            const uint64_t p2 = pack2(pu, pu);
-            acc[h][0] = ffma2(p2, vx[u].x, acc[h][0]);
-            acc[h][1] = ffma2(p2, vx[u].y, acc[h][1]);
+      for (int u = 0; u < 8; ++u) {
+        const ulonglong2 vx = *reinterpret_cast<const ulonglong2*>(&sm.kv[1][u][tid]);
+        const ulonglong2* pp = reinterpret_cast<const ulonglong2*>(sm.p[warp][grp][u]);
+#pragma unroll
+        for (int h = 0; h < G; h += 2) {
+          const ulonglong2 w = pp[h / 2];
+          acc[h][0] = ffma2(w.x, vx.x, acc[h][0]);
+          acc[h][1] = ffma2(w.x, vx.y, acc[h][1]);
+          if (h + 1 < G) {
+            acc[h + 1 < G ? h + 1 : h][0] = ffma2(w.y, vx.x, acc[h + 1 < G ? h + 1 : h][0]);
+            acc[h + 1 < G ? h + 1 : h][1] = ffma2(w.y, vx.y, acc[h + 1 < G ? h + 1 : h][1]);
           }
         }
       }
+      __syncwarp();                                 // sm.p has been read
+      if (more) copy(next, 1);
+      commit();
+      cur = next;
+      if (i + 2 * NW < nunits) next = span(i + 2 * NW);
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();                                // sm.kv has been read
     // ---- the groups of lanes, then the warps
 #pragma unroll
     for (int h = 0; h < G; ++h) {
@@ -155,6 +203,7 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
       // one lane of each key
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], LPR / 2);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], LPR / 4);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], LPR / 8);
       if (grp == 0) *reinterpret_cast<float4*>(&sm.o[warp][h][4 * lr]) = o;
       if (lane == 0) {
         sm.m[warp][h] = m[h];
