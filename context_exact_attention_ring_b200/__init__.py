@@ -15,7 +15,7 @@ Names follow the C ABI:
   ring_attn_kv_append, ring_attn_sched_stats, ring_attn_device_error;
   ring_attn_page_extend, ring_attn_page_trim, ring_attn_paged_append,
   ring_attn_decode_paged, ring_attn_page_bounds, ring_attn_page_scores,
-  ring_attn_page_select (the paged KV cache);
+  ring_attn_page_select, ring_attn_paged_packed (the paged KV cache);
 and ring_attention (RingAttnFunction), the forward and backward under autograd.
 """
 from __future__ import annotations
@@ -23,6 +23,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -49,6 +50,7 @@ EXPORTED = (
     "ring_attn_bwd_workspace_bytes", "ring_attn_step_bwd", "ring_attn_bwd_simt",
     "ring_attn_page_extend", "ring_attn_page_trim", "ring_attn_paged_append", "ring_attn_decode_paged_workspace_bytes",
     "ring_attn_decode_paged", "ring_attn_page_bounds", "ring_attn_page_scores", "ring_attn_page_select",
+    "ring_attn_paged_packed",
 )
 
 
@@ -108,6 +110,7 @@ def lib():
         "ring_attn_page_bounds": [vp] * 5 + [i32] * 6 + [sz] * 4 + [i32, vp],
         "ring_attn_page_scores": [vp] * 5 + [i32] * 7 + [sz] * 3 + [i32, vp],
         "ring_attn_page_select": [vp] * 4 + [i32] * 7 + [vp],
+        "ring_attn_paged_packed": [i32, vp, i32, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -498,14 +501,23 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+# RING_PAGE_EXTEND .. RING_PAGE_SELECT: the calls of ring_attn_paged_packed and their arguments' packing
+_PACKED = {name: (i, struct.Struct(words), words.count("q") + words.count("d")) for i, (name, words) in enumerate((
+    ("ring_attn_page_extend", "q" * 14), ("ring_attn_page_trim", "q" * 10), ("ring_attn_paged_append", "q" * 16),
+    ("ring_attn_decode_paged", "q" * 23 + "d" + "q" * 4), ("ring_attn_page_bounds", "q" * 16),
+    ("ring_attn_page_scores", "q" * 16), ("ring_attn_page_select", "q" * 11)))}
+
+
 def _launch(name, dev, *args):
     """Call the library on the tensors' device, on that device's current torch stream."""
-    fn = getattr(_lib or lib(), name)
+    call, words, n = _PACKED[name]
+    fn = (_lib or lib()).ring_attn_paged_packed
+    packed = words.pack(*args)
     if torch.cuda.current_device() == dev:
-        st = fn(*args, _raw_stream(dev))
+        st = fn(call, packed, n, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _raw_stream(dev))
+            st = fn(call, packed, n, _raw_stream(dev))
     if st != RING_OK:
         _check(st, name)
 
@@ -628,7 +640,7 @@ def ring_attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, sel=None, n
     tp, W, ts = _table(block_table, B)
     if (sel is None) != (n_sel is None):
         raise ValueError("give both sel and n_sel, or neither")
-    K, selp, nselp = 0, None, None
+    K, selp, nselp = 0, 0, 0
     if sel is not None:
         K = sel.shape[-1] if sel.dim() else 0
         selp, nselp = _int32("sel", sel, (B, Hkv, K)), _int32("n_sel", n_sel, (B, Hkv))
@@ -666,7 +678,7 @@ def ring_attn_page_bounds(k_pool, block_table, seq_lens, bounds=None, start_lens
         raise ValueError("bounds must be contiguous [num_pages, Hkv, 2, D] of the cache's dtype")
     _launch("ring_attn_page_bounds", dev, k_pool.data_ptr(), bounds.data_ptr(), tp,
             _int32("seq_lens", seq_lens, (B,)),
-            None if start_lens is None else _int32("start_lens", start_lens, (B,)), B, Hkv, D, N, ps, W, sp, st, sh,
+            0 if start_lens is None else _int32("start_lens", start_lens, (B,)), B, Hkv, D, N, ps, W, sp, st, sh,
             ts, _dtype_code(k_pool))
     return bounds
 

@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "../../include/ring_attn.h"
 #include "kernels.h"
@@ -231,6 +232,52 @@ ring_status ring_attn_page_select(const float* scores, const int32_t* seq_lens, 
   if (!table_fits(W, pl) || (long long)B * Hkv > 0x7fffffffLL) return RING_EINVAL;
   SelectArgs a{scores, seq_lens, sel, n_sel, B, Hkv, W, pl, K, keep_first, keep_last};
   return from_cuda(launch_page_select(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ring_status ring_attn_paged_packed(int call, const int64_t* args, int n, void* stream) {
+  if (!args || (reinterpret_cast<uintptr_t>(args) & 7u)) return RING_EINVAL;
+  // the arguments in order: pointers, ints and sizes as they are, the scale as the bits of a double
+  auto ptr = [&](int i) { return reinterpret_cast<void*>(static_cast<intptr_t>(args[i])); };
+  auto i32 = [&](int i) { return reinterpret_cast<int32_t*>(ptr(i)); };
+  auto f32 = [&](int i) { return reinterpret_cast<float*>(ptr(i)); };
+  auto num = [&](int i) { return static_cast<int>(args[i]); };
+  auto size = [&](int i) { return static_cast<size_t>(args[i]); };
+  switch (call) {
+    case RING_PAGE_EXTEND:
+      if (n != 14) return RING_EINVAL;
+      return ring_attn_page_extend(i32(0), i32(1), i32(2), i32(3), i32(4), i32(5), i32(6), i32(7), num(8), num(9),
+                                   size(10), num(11), num(12), num(13), stream);
+    case RING_PAGE_TRIM:
+      if (n != 10) return RING_EINVAL;
+      return ring_attn_page_trim(i32(0), i32(1), i32(2), i32(3), i32(4), num(5), num(6), size(7), num(8), num(9),
+                                 stream);
+    case RING_PAGED_APPEND:
+      if (n != 16) return RING_EINVAL;
+      return ring_attn_paged_append(ptr(0), ptr(1), ptr(2), ptr(3), i32(4), num(5), num(6), num(7), num(8), num(9),
+                                    size(10), size(11), size(12), size(13), size(14), num(15), stream);
+    case RING_DECODE_PAGED: {
+      if (n != 28) return RING_EINVAL;
+      double scale;
+      memcpy(&scale, args + 23, sizeof(scale));
+      return ring_attn_decode_paged(ptr(0), ptr(1), ptr(2), i32(3), i32(4), i32(5), i32(6), ptr(7), f32(8), num(9),
+                                    num(10), num(11), num(12), num(13), num(14), num(15), num(16), size(17), size(18),
+                                    size(19), size(20), size(21), size(22), static_cast<float>(scale), num(24), num(25),
+                                    ptr(26), size(27), stream);
+    }
+    case RING_PAGE_BOUNDS:
+      if (n != 16) return RING_EINVAL;
+      return ring_attn_page_bounds(ptr(0), ptr(1), i32(2), i32(3), i32(4), num(5), num(6), num(7), num(8), num(9),
+                                   num(10), size(11), size(12), size(13), size(14), num(15), stream);
+    case RING_PAGE_SCORES:
+      if (n != 16) return RING_EINVAL;
+      return ring_attn_page_scores(ptr(0), ptr(1), i32(2), i32(3), f32(4), num(5), num(6), num(7), num(8), num(9),
+                                   num(10), num(11), size(12), size(13), size(14), num(15), stream);
+    case RING_PAGE_SELECT:
+      if (n != 11) return RING_EINVAL;
+      return ring_attn_page_select(f32(0), i32(1), i32(2), i32(3), num(4), num(5), num(6), num(7), num(8), num(9),
+                                   num(10), stream);
+  }
+  return RING_EINVAL;
 }
 
 }  // extern "C"

@@ -56,7 +56,7 @@ constexpr uint32_t TMEM_COLS = 128;         // S^T 2 x 16, O^T 2 x (16 or 32)
 constexpr float LAZY = 8.f;                 // log2 of the growth tolerated before the base moves
 constexpr int MAX_SLOTS = kPagedTile / 8;   // page slots of a tile
 constexpr int SEG_COST = 1;                 // what a segment costs besides its tiles, in tiles
-constexpr int PARTS_PER_TILE = 10;          // parts joined in the time of a tile
+constexpr int PARTS_PER_TILE = 20;          // parts joined in the time of a tile
 }  // namespace pdt
 
 template <int G, int DH>

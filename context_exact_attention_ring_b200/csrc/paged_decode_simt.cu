@@ -28,7 +28,7 @@ constexpr int THREADS = 512;
 constexpr int NW = THREADS / 32;
 constexpr int HEADS = 8;               // query heads of a group, at most
 constexpr int SEG_COST = 1;            // what a segment costs besides its tiles, in tiles
-constexpr int PARTS_PER_TILE = 10;     // parts joined in the time of a tile
+constexpr int PARTS_PER_TILE = 20;     // parts joined in the time of a tile
 }  // namespace pds
 
 template <int G, int D>

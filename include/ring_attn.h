@@ -593,6 +593,24 @@ ring_status ring_attn_page_scores(const void* q, const void* bounds, const int32
 ring_status ring_attn_page_select(const float* scores, const int32_t* seq_lens, int32_t* sel, int32_t* n_sel, int B,
                                   int Hkv, int W, int page_size, int K, int keep_first, int keep_last, void* stream);
 
+/* The calls ring_attn_paged_packed makes. */
+typedef enum {
+  RING_PAGE_EXTEND = 0, RING_PAGE_TRIM = 1, RING_PAGED_APPEND = 2, RING_DECODE_PAGED = 3, RING_PAGE_BOUNDS = 4,
+  RING_PAGE_SCORES = 5, RING_PAGE_SELECT = 6
+} ring_paged_call;
+
+/*
+ * ring_attn_paged_packed -- one of the paged-cache calls above, its arguments
+ * but the stream packed in order into n 64-bit words: pointers, integers and
+ * sizes by value, the scale as a double.  For bindings that pay for every
+ * argument (ctypes takes 2.4 us for ring_attn_decode_paged's, 1.1 us packed).
+ * args is host memory, read before the call returns.
+ * Returns what the call returns; RING_EINVAL for an unknown call, a null or
+ * misaligned args, or another number of words than the call has arguments.
+ * The source pages have no counterpart.
+ */
+ring_status ring_attn_paged_packed(int call, const int64_t* args, int n, void* stream);
+
 /*
  * ring_attn_sched_stats -- the scheduler's host-side view of one (batch, head)
  * of a causal or full ring, without running anything: per-rank unmasked

@@ -165,3 +165,28 @@ def test_binding_passes_strides_of_views(as_if_on_gpu):
     ra.ring_attn_paged_append(one, one, one[0], one[0], ints(16))
     name, args = as_if_on_gpu.pop()
     assert args[10:15] == (1024, 64, 64, 64, 64)
+
+
+PACKED = [("ring_attn_page_extend", EXTEND), ("ring_attn_page_trim", TRIM), ("ring_attn_paged_append", APPEND),
+          ("ring_attn_decode_paged", DECODE), ("ring_attn_page_bounds", BOUNDS), ("ring_attn_page_scores", SCORES),
+          ("ring_attn_page_select", SELECT)]
+
+
+@pytest.mark.parametrize("i,name,base", [(i, n, b) for i, (n, b) in enumerate(PACKED)])
+def test_packed_calls_take_their_arguments_in_order(i, name, base):
+    # every argument that the flat call refuses is refused in its place of the packed words
+    import ctypes
+    call_no, words, n = ra._PACKED[name]
+    assert call_no == i and n == len(base) == words.size // 8
+    assert len(ra._PACKED) == len(PACKED)
+    fn = ra.lib().ring_attn_paged_packed
+    for nm, b, kw, code in CASES:
+        if nm == name:
+            packed = words.pack(*[0 if v is None else v for v in {**b, **kw}.values()])
+            assert fn(i, packed, n, None) == code, kw
+    packed = words.pack(*[0 if v is None else v for v in base.values()])
+    assert fn(i, packed, n - 1, None) == E and fn(i, None, n, None) == E
+    assert fn(len(PACKED), packed, n, None) == E and fn(-1, packed, n, None) == E
+    buf = ctypes.create_string_buffer(packed + b"\0" * 16)
+    at = ctypes.addressof(buf)
+    assert fn(i, at + 4 - at % 4, n, None) == E if (at + 4 - at % 4) % 8 else True
