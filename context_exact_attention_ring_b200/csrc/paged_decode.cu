@@ -155,26 +155,14 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
   const int psn_log2 = min(a.ps_log2, 7), psn = 1 << psn_log2;   // rows of a page slot
 
   paged_begin();
-  const int mine = paged_first_tiles(a);   // on its way during the setup
+  // few rows: every warp plans by itself, and the producers start while the others set up
+  const bool few = rows.R <= 32;
+  const int mine = !few ? paged_first_tiles(a) : lane < rows.R ? paged_tiles(a, lane) : 0;   // on its way meanwhile
   if (threadIdx.x == 4 * 32) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
   }
   if (threadIdx.x == 6 * 32) tma_prefetch_desc(&tmV);
-
-  // padded query rows and weight columns stay zero
-  {
-    uint4* z = reinterpret_cast<uint4*>(&sm.q[0][0]);
-    constexpr int n16 = (int)((sizeof(sm.q) + sizeof(sm.pt)) / 16);
-    for (int i = threadIdx.x; i < n16; i += THREADS) z[i] = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (DH == 64)
-      // the second 64 columns of V: the upper half of M = 128 dims, zero
-      for (int st = 0; st < NST; ++st) {
-        uint4* zv = reinterpret_cast<uint4*>(sm.kv[st][1] + SLAB);
-        for (int i = threadIdx.x; i < SLAB / 16; i += THREADS) zv[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    fence_proxy_async_smem();
-  }
   if (warp == 0) {
     // a lane per barrier; those the softmax threads arrive on count all of them
     constexpr int NB = 4 * NST + 17;
@@ -188,15 +176,35 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == 5) {
-    tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  const PagedRun run = paged_run<THREADS>(a, sm.run, mine, SEG_COST, PARTS_PER_TILE);   // synchronises the CTA
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  const PagedRun run = few ? paged_run_warp(a, mine, SEG_COST, PARTS_PER_TILE)
+                           : paged_run<THREADS>(a, sm.run, mine, SEG_COST, PARTS_PER_TILE);
+  uint32_t tmem = 0;
+  if (warp != 4 && warp != 6) {
+    // the query rows past the box, all weight columns and, for D = 64, the second 64 columns of V (the
+    // upper half of M = 128 dims) are zero: never written by the copies
+    constexpr int NT = THREADS - 64;
+    const int tid = warp == 5 ? CT + lane : threadIdx.x;
+    uint4* z = reinterpret_cast<uint4*>(&sm.q[0][0]);
+    for (int i = tid; i < (int)sizeof(sm.q) / 16; i += NT)
+      if ((i >> 3) % NQ >= maps.q_rows) z[i] = make_uint4(0u, 0u, 0u, 0u);
+    z = reinterpret_cast<uint4*>(&sm.pt[0][0]);
+    for (int i = tid; i < (int)sizeof(sm.pt) / 16; i += NT) z[i] = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (DH == 64)
+      for (int st = 0; st < NST; ++st) {
+        z = reinterpret_cast<uint4*>(sm.kv[st][1] + SLAB);
+        for (int i = tid; i < SLAB / 16; i += NT) z[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    fence_proxy_async_smem();
+    if (warp == 5) {
+      tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    named_bar_sync(2, NT);
+    tc_fence_after();
+    tmem = sm.tmem_base;
+  }
 
   if (warp == 4 || warp == 6) {
     // ------------------------------------------------------------ producers

@@ -69,10 +69,22 @@ struct PagedRunSmem {
   int row, row_t;
 };
 
-// All threads of the CTA (a multiple of 32, at most 1024).
+// The number of CTAs for run.T units in segs segments, and this CTA's run.
 // parts_per_tile: how many parts a segment may be cut into for every tile of
 // a part.  Joining takes as long as a tile for every parts_per_tile parts, so
 // that cutting n parts of T / n tiles is longest at n^2 = parts_per_tile T.
+__device__ __forceinline__ void paged_cut(PagedRun& run, int segs, int seg_cost, int parts_per_tile) {
+  const int tiles = run.T - segs * seg_cost, c = blockIdx.x;
+  run.n = max(1, min(min((int)gridDim.x, tiles), (int)sqrtf((float)parts_per_tile * tiles * segs)));
+  run.row = run.row_t = run.q = run.r = run.t0 = run.t1 = 0;
+  if (run.T == 0 || c >= run.n) return;
+  run.q = run.T / run.n;
+  run.r = run.T - run.n * run.q;
+  run.t0 = run_start(run, c);
+  run.t1 = run_start(run, c + 1);
+}
+
+// The plan by all threads of the CTA (a multiple of 32, at most 1024).
 // mine: the tiles of row threadIdx.x (paged_first_tiles), loaded earlier.
 __device__ __forceinline__ int paged_first_tiles(const PagedDecodeArgs& a) {
   return (int)threadIdx.x < paged_rows(a).R ? paged_tiles(a, threadIdx.x) : 0;
@@ -119,19 +131,8 @@ __device__ __forceinline__ PagedRun paged_run(const PagedDecodeArgs& a, PagedRun
   }
   PagedRun run;
   run.T = (units + more) * rows.mult;
-  segs *= rows.mult;
-  const int tiles = run.T - segs * seg_cost;
-  run.n = max(1, min(min((int)gridDim.x, tiles), (int)sqrtf((float)parts_per_tile * tiles * segs)));
-  run.row = run.row_t = run.q = run.r = 0;
-  const int c = blockIdx.x;
-  if (run.T == 0 || c >= run.n) {
-    run.t0 = run.t1 = 0;
-    return run;
-  }
-  run.q = run.T / run.n;
-  run.r = run.T - run.n * run.q;
-  run.t0 = run_start(run, c);
-  run.t1 = run_start(run, c + 1);
+  paged_cut(run, segs * rows.mult, seg_cost, parts_per_tile);
+  if (run.t0 == run.t1) return run;
   // the row that holds t0
   const int want = run.t0 / rows.mult;    // units counted once per row
   int hi = before + incl0, lo = hi - units0, base = units;
@@ -162,6 +163,31 @@ __device__ __forceinline__ PagedRun paged_run(const PagedDecodeArgs& a, PagedRun
   __syncthreads();
   run.row = s.row;
   run.row_t = s.row_t;
+  return run;
+}
+
+// The same for at most 32 rows, by every warp on its own (no barrier): mine is
+// the tiles of row `lane`.
+__device__ __forceinline__ PagedRun paged_run_warp(const PagedDecodeArgs& a, int mine, int seg_cost,
+                                                   int parts_per_tile) {
+  const int lane = threadIdx.x & 31;
+  const PagedRows rows = paged_rows(a);
+  const int nu = paged_units(mine, seg_cost);
+  int hi = nu;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, hi, o);
+    if (lane >= o) hi += up;
+  }
+  PagedRun run;
+  const int segs = __popc(__ballot_sync(0xffffffffu, mine > 0)) * rows.mult;
+  run.T = __shfl_sync(0xffffffffu, hi, 31) * rows.mult;
+  paged_cut(run, segs, seg_cost, parts_per_tile);
+  if (run.t0 < run.t1) {
+    const int want = run.t0 / rows.mult;
+    run.row = __ffs(__ballot_sync(0xffffffffu, want < hi)) - 1;      // the first whose units end past it
+    run.row_t = __shfl_sync(0xffffffffu, hi - nu, run.row) * rows.mult;
+  }
   return run;
 }
 
