@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(pgt::THREADS, 1) page_extend_kernel(ExtendArgs
     const long long cu1 = tokens + block_scan(add, s.warp, &total);
     const long long cu0 = cu1 - add;
     tokens += total;
-    const bool fits = in && len + add <= cap && cu1 <= a.max_tokens;
+    const bool fits = in && len + add <= cap && (add == 0 || cu1 <= a.max_tokens);
     const int old = pages_of(len, a.ps_log2);
     const int need = fits ? pages_of(len + add, a.ps_log2) - old : 0;
     const long long upto = block_scan(need, s.warp, &total);

@@ -450,8 +450,8 @@ ring_status ring_attn_kv_append(void* k_cache, void* v_cache, const void* k_new,
  * A sequence is left as it was (start_lens -1) if its new length exceeds
  * W*page_size, if its tokens pass max_tokens, or if the free list does not
  * hold its pages after those of the sequences before it (a sequence that
- * needs no new page is served all the same); ring_attn_device_error() then
- * reports RING_ECAPACITY.  Entries of block_table that are not taken into use
+ * needs no new page, or gets no token, is served all the same);
+ * ring_attn_device_error() then reports RING_ECAPACITY.  Entries of block_table that are not taken into use
  * keep their value.  The page numbers themselves are not checked here.
  * Returns RING_EINVAL for null/misaligned pointers, sizes < 1, table_stride <
  * W or W*page_size beyond 32 bits; RING_EUNSUPPORTED for a page size that is
@@ -472,7 +472,9 @@ ring_status ring_attn_page_extend(int32_t* seq_lens, const int32_t* new_lens, in
  * by some tokens and cutting the same tokens off again restores the list.
  * free_pages has room for max_free pages; what would pass that is dropped and
  * ring_attn_device_error() reports RING_ECAPACITY.  block_table is not
- * changed.  Errors as ring_attn_page_extend.
+ * changed.  A page in two sequences' tables is given back once for each: where
+ * sequences share pages, the caller keeps count.
+ * Errors as ring_attn_page_extend.
  * The source pages have no counterpart.
  */
 ring_status ring_attn_page_trim(int32_t* seq_lens, const int32_t* keep_lens, const int32_t* block_table,
@@ -519,7 +521,7 @@ size_t ring_attn_decode_paged_workspace_bytes(int D);
  * nothing, and a page listed twice counts twice.  A row without a key gives
  * out = 0, lse = -inf.  Keys past the length may hold anything.
  * The float32 out with out_lse of a shard of a sequence can be merged with
- * other shards' by ring_attn_merge.
+ * other shards' by ring_attn_merge.  out may not overlap q.
  * workspace: ring_attn_decode_paged_workspace_bytes(D) bytes, 256-byte
  * aligned; its counters must be zero before the first call on it and every
  * call that completes leaves them zero (after RING_ETIMEOUT, zero it again).

@@ -24,7 +24,7 @@ class Tables:
             new = max(0, int(new))
             cu.append(cu[-1] + new)
             old = min(max(self.lens[b], 0), W * ps)
-            if old + new > W * ps or cu[-1] > max_tokens:
+            if old + new > W * ps or (new and cu[-1] > max_tokens):
                 start.append(-1)
                 short = True
                 continue

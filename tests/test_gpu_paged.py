@@ -41,6 +41,7 @@ def _tables(lens, ps, W, extra, seed):
 @pytest.mark.parametrize("ps", [8, 16, 1024])
 @pytest.mark.parametrize("B,news,max_tokens", [
     (1, [0], 1), (1, [1], 1), (5, [3, 0, 17, 1, 40], 64), (5, [-4, 2000, 1, 1, 9], 5000), (6, [5, 5, 5, 5, 5, 5], 30),
+    (6, [5, 40, 0, 3, 0, 1], 40),                        # tokens past the slot map; those without any are served
 ])
 def test_extend_and_trim_small(ps, B, news, max_tokens):
     need_cuda()
@@ -307,6 +308,7 @@ def test_decode_selected_pages(dtype, Hq, Hkv, D, ps, K):
     sel[3, 0, 1] = sel[3, 0, 0]                          # a page twice counts twice
     sel[3, 1, :2] = [-3, 10 ** 6]                        # outside the sequence: ignored
     n_sel[0, 1] = 0                                      # one head of a sequence reads nothing
+    sel[2, 0, :2], n_sel[2, 0] = [0, 1], 2               # pages listed of an empty sequence
     n_sel[3, Hkv - 1] = K + 100                          # clamped to K
     out, lse = ra.ring_attn_decode_paged(q, k, v, tb, ints(lens), sel=ints(sel), n_sel=ints(n_sel))
     ok()
