@@ -646,11 +646,12 @@ def ring_attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, sel=None, n
         selp, nselp = _int32("sel", sel, (B, Hkv, K)), _int32("n_sel", n_sel, (B, Hkv))
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     if out is None:
-        out = q.new_empty((B, Hq, D), dtype=out_dtype or q.dtype)
+        # (new_empty_strided takes two thirds of new_empty's time)
+        out = q.new_empty_strided((B, Hq, D), (Hq * D, D, 1), dtype=out_dtype or q.dtype)
     elif tuple(out.shape) != (B, Hq, D) or not out.is_contiguous() or (out_dtype or out.dtype) != out.dtype:
         raise ValueError("out must be contiguous [B, Hq, D] of out_dtype")
     if out_lse is None:
-        out_lse = q.new_empty((B, Hq), dtype=torch.float32)
+        out_lse = q.new_empty_strided((B, Hq), (Hq, 1), dtype=torch.float32)
     elif tuple(out_lse.shape) != (B, Hq) or out_lse.dtype != torch.float32 or not out_lse.is_contiguous():
         raise ValueError("out_lse must be contiguous float32 [B, Hq]")
     if workspace is None:
@@ -712,9 +713,9 @@ def ring_attn_page_select(scores, seq_lens, page_size, K, keep_first=1, keep_las
     B, Hkv, W = scores.shape
     K = int(K)
     if sel is None:
-        sel = seq_lens.new_empty((B, Hkv, K), dtype=torch.int32)
+        sel = seq_lens.new_empty_strided((B, Hkv, K), (Hkv * K, K, 1), dtype=torch.int32)
     if n_sel is None:
-        n_sel = seq_lens.new_empty((B, Hkv), dtype=torch.int32)
+        n_sel = seq_lens.new_empty_strided((B, Hkv), (Hkv, 1), dtype=torch.int32)
     _launch("ring_attn_page_select", dev, scores.data_ptr(), _int32("seq_lens", seq_lens, (B,)),
             _int32("sel", sel, (B, Hkv, K)), _int32("n_sel", n_sel, (B, Hkv)), B, Hkv, W, int(page_size), K,
             int(keep_first), int(keep_last))

@@ -190,3 +190,40 @@ def test_packed_calls_take_their_arguments_in_order(i, name, base):
     buf = ctypes.create_string_buffer(packed + b"\0" * 16)
     at = ctypes.addressof(buf)
     assert fn(i, at + 4 - at % 4, n, None) == E if (at + 4 - at % 4) % 8 else True
+
+
+class _Fake:
+    def __init__(self, dev):
+        self.dev = dev
+
+    def get_device(self):
+        return self.dev
+
+
+def test_tensors_of_one_device_and_its_stream(monkeypatch):
+    assert ra._one_device(_Fake(1), None, _Fake(1)) == 1
+    for devs in ((0, 1), (-1,), (0, -1), (-1, 0)):
+        with pytest.raises(ValueError, match="device"):
+            ra._one_device(*(_Fake(d) for d in devs))
+    # a call on tensors of another device than the current one switches to it, and takes its stream
+    import contextlib
+    seen, current = [], [0]
+
+    class Lib:
+        def ring_attn_paged_packed(self, call, words, n, stream):
+            seen.append((call, n, stream, current[0]))
+            return 0
+
+    @contextlib.contextmanager
+    def device(d):
+        old, current[0] = current[0], d
+        yield
+        current[0] = old
+
+    monkeypatch.setattr(ra, "_lib", Lib())
+    monkeypatch.setattr(ra, "_raw_stream", lambda d: 1000 + d)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    ra._launch("ring_attn_page_select", 0, *range(11))
+    ra._launch("ring_attn_page_select", 2, *range(11))
+    assert seen == [(6, 11, 1000, 0), (6, 11, 1002, 2)] and current == [0]
