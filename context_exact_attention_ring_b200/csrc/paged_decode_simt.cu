@@ -14,7 +14,8 @@
 // key), so that a lane takes one maximum and one exponential per head; the
 // weights return through shared memory as pairs.  Bound by instructions, about
 // 85 per head and 8 keys of a group, above two heads, and by memory below.
-// (Four keys at a time: 62 us for 400,000 rows of 5 heads of 64, eight: 57.)
+// (Four keys at a time: 62 us for 400,000 rows of 5 heads of 64, eight: 57, with
+// the runs weighed as now 48.)
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -27,7 +28,9 @@ namespace pds {
 constexpr int THREADS = 512;
 constexpr int NW = THREADS / 32;
 constexpr int HEADS = 8;               // query heads of a group, at most
-constexpr int SEG_COST = 1;            // what a segment costs besides its tiles, in tiles
+// What a segment costs besides its tiles (queries, the empty pipeline, the warps' sums), in tiles; with 1
+// the case of 5 heads took 57 us, with 2 and 3 it takes 48.
+constexpr int SEG_COST = 2;
 constexpr int PARTS_PER_TILE = 20;     // parts joined in the time of a tile
 }  // namespace pds
 
@@ -65,9 +68,10 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
   const PagedRun run = paged_run<THREADS>(a, sm.run, paged_first_tiles(a), SEG_COST, PARTS_PER_TILE);
   paged_empty_rows(a, tid, THREADS);
   const float sl2 = a.scale * 1.4426950408889634f;
-  // after the exchanges a lane holds key `mine` of its group's eight
-  const bool b2 = lr & (LPR / 2), b1 = lr & (LPR / 4), b0 = lr & (LPR / 8);
-  const int mine = (b2 ? 4 : 0) + (b1 ? 2 : 0) + (b0 ? 1 : 0);
+  // A lane takes its group's eight keys in the order u ^ mine, u = 0 .. 7.  A lane that differs from it
+  // in one bit of `mine` then has the sum for the lane's place u at its own place u + 4 (2, 1): halving
+  // needs no selection, and ends with key `mine` in place 0.
+  const int mine = (lr & (LPR / 2) ? 4 : 0) + (lr & (LPR / 4) ? 2 : 0) + (lr & (LPR / 8) ? 1 : 0);
   PagedWalk walk(a, rows, run, SEG_COST);
   PagedPiece pc;
   while (walk.next(a, rows, pc)) {
@@ -97,11 +101,8 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
                           (size_t)hd.g * a.pool.head + 4 * lr;
       const float* row = static_cast<const float*>(which ? a.v : a.k) + base;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const bool ok = u < sp.valid;
-        copy16(&sm.kv[which][u][tid], row, ok);
-        if (ok) row += a.pool.token;
-      }
+      for (int u = 0; u < 8; ++u, row += a.pool.token)      // rows of one page, valid or not
+        copy16(&sm.kv[which][u][tid], row, u < sp.valid);
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
     PagedSpan cur, next;
@@ -124,25 +125,19 @@ __global__ void __launch_bounds__(pds::THREADS, 1) paged_decode_simt_kernel(Page
       {
         ulonglong2 kx[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) kx[u] = *reinterpret_cast<const ulonglong2*>(&sm.kv[0][u][tid]);
+        for (int u = 0; u < 8; ++u) kx[u] = *reinterpret_cast<const ulonglong2*>(&sm.kv[0][u ^ mine][tid]);
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&sm.q[h][4 * lr]);
           float s[8];
 #pragma unroll
           for (int u = 0; u < 8; ++u) s[u] = hsum2(ffma2(q.x, kx[u].x, fmul2(q.y, kx[u].y)));
-          // keep half of the keys and send the sums of the others, three times
+          // keep the lower half of the places and send the sums of the upper, three times
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float keep = b2 ? s[4 + u] : s[u], send = b2 ? s[u] : s[4 + u];
-            s[u] = keep + __shfl_xor_sync(0xffffffffu, send, LPR / 2);
-          }
+          for (int u = 0; u < 4; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[4 + u], LPR / 2);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float keep = b1 ? s[2 + u] : s[u], send = b1 ? s[u] : s[2 + u];
-            s[u] = keep + __shfl_xor_sync(0xffffffffu, send, LPR / 4);
-          }
-          float x = (b0 ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, b0 ? s[0] : s[1], LPR / 8);
+          for (int u = 0; u < 2; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[2 + u], LPR / 4);
+          float x = s[0] + __shfl_xor_sync(0xffffffffu, s[1], LPR / 8);
 #pragma unroll
           for (int o = LPR / 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
           if (!valid) x = -CUDART_INF_F;
