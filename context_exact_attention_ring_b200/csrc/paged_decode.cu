@@ -18,7 +18,8 @@
 //   warps 4, 6 producers of K (and Q) and of V: lane i owns page slot i of a
 //              tile (a tile holds 128 / page_size pages, or is part of one)
 //              and looks its page up one tile ahead; each lane issues its
-//              page's TMA boxes into a ring of 3 stages.  Issuing a box takes
+//              page's TMA boxes into a ring of 3 stages (5 at
+//              D = 64).  Issuing a box takes
 //              60-80 cycles (120 if one lane does it for all), and a tile of
 //              16-token pages is 32 boxes in the 2700 cycles its bytes take:
 //              hence two warps.  The V producer
@@ -46,16 +47,22 @@ namespace ra {
 
 namespace pdt {
 constexpr int NQ = 16;                      // heads per CTA, padded
-constexpr int NST = 3;                      // K/V stages
 constexpr int SLAB = kPagedTile * 128;      // 128 rows x 64 columns of bf16 (16 KB)
-constexpr int TILE_BYTES = 2 * SLAB;        // one K or V tile
 constexpr int QSLAB = NQ * 128;
 constexpr int CT = 128;                     // softmax threads
 constexpr int THREADS = CT + 96;
 constexpr uint32_t TMEM_COLS = 128;         // S^T 2 x 16, O^T 2 x (16 or 32)
 constexpr float LAZY = 8.f;                 // log2 of the growth tolerated before the base moves
+// K/V stages: what shared memory holds.  A V tile stays until its product is done, twice its flight time
+// at D = 64, where three stages of half the bytes reached 0.68 of the copy rate.
+template <int DH>
+constexpr int NST = DH == 64 ? 5 : 3;
 constexpr int MAX_SLOTS = kPagedTile / 8;   // page slots of a tile
-constexpr int SEG_COST = 1;                 // what a segment costs besides its tiles, in tiles
+// What a segment costs besides its tiles, in tiles: its result's sums, divisions and stores grow with the
+// heads (64 ragged sequences with 16 heads to a kv head: 129 us with 1, 111 with 2; with 4 heads 103 and 103,
+// 128 shorter ones 54 and 57).
+template <int G>
+constexpr int SEG_COST = G > 8 ? 2 : 1;
 constexpr int PARTS_PER_TILE = 20;          // parts joined in the time of a tile
 }  // namespace pdt
 
@@ -64,16 +71,19 @@ struct PagedSmem {
   static constexpr int GP = G <= 8 ? 8 : 16;  // weight columns of a term
   static constexpr int NP = 2 * GP;           // weight columns: hi, lo
   static constexpr int PSLAB = NP * 128;      // 64 keys of all weight columns
-  alignas(1024) uint8_t kv[pdt::NST][2][pdt::TILE_BYTES];
+  static constexpr int NST = pdt::NST<DH>;
+  alignas(1024) uint8_t kv[NST][2][(DH / 64) * pdt::SLAB];
+  // D = 64: the upper 64 of the M = 128 dims of O^T, common to all stages
+  alignas(1024) uint8_t zero[DH == 64 ? pdt::SLAB : 1];
   alignas(1024) uint8_t q[2][2 * pdt::QSLAB];
   alignas(1024) uint8_t pt[2][2 * PSLAB];
-  int nvalid[pdt::NST][pdt::MAX_SLOTS];       // valid keys per page slot of a V stage
+  int nvalid[NST][pdt::MAX_SLOTS];       // valid keys per page slot of a V stage
   alignas(16) float red[2][GP][4];            // the warps' maxima, by tile parity
   alignas(16) float suml[2][GP][4];           // the warps' sums, by piece parity
   float base[2][GP];                          // final bases
   alignas(16) typename PagedJoin<pdt::CT, G, DH>::Smem join;
   // mbarriers
-  alignas(8) uint64_t k_full[pdt::NST], k_empty[pdt::NST], v_full[pdt::NST], v_empty[pdt::NST];
+  alignas(8) uint64_t k_full[NST], k_empty[NST], v_full[NST], v_empty[NST];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], s_free[2], o_done[2], o_full[2], o_free[2], teardown;
   PagedRunSmem run;
   uint32_t tmem_base;
@@ -145,7 +155,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
                         const __grid_constant__ CUtensorMap tmV, PagedDecodeArgs a, PagedMaps maps) {
   using namespace pdt;
   using Smem = PagedSmem<G, DH>;
-  constexpr int GP = Smem::GP, NP = Smem::NP, PSLAB = Smem::PSLAB;
+  constexpr int GP = Smem::GP, NP = Smem::NP, PSLAB = Smem::PSLAB, NST = Smem::NST;
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -164,25 +174,23 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
   }
   if (threadIdx.x == 6 * 32) tma_prefetch_desc(&tmV);
   if (warp == 0) {
-    // a lane per barrier; those the softmax threads arrive on count all of them
-    constexpr int NB = 4 * NST + 17;
-    static_assert(NB <= 32, "a lane per barrier");
-    const uint32_t first = smem_u32(&sm.k_full[0]);
-    const uint32_t bar = first + 8 * lane;
-    const bool by_all = (bar >= smem_u32(&sm.p_full[0]) && bar < smem_u32(&sm.o_done[0])) ||
-                        (bar >= smem_u32(&sm.o_free[0]) && bar < smem_u32(&sm.teardown));
-    if (lane < NB) mbar_init(bar, by_all ? CT : 1);
+    // a barrier per lane at a time; those the softmax threads arrive on count all of them
+    for (uint32_t bar = smem_u32(&sm.k_full[0]) + 8 * lane; bar <= smem_u32(&sm.teardown); bar += 8 * 32) {
+      const bool by_all = (bar >= smem_u32(&sm.p_full[0]) && bar < smem_u32(&sm.o_done[0])) ||
+                          (bar >= smem_u32(&sm.o_free[0]) && bar < smem_u32(&sm.teardown));
+      mbar_init(bar, by_all ? CT : 1);
+    }
     if (lane == 0) sm.abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
   __syncthreads();
-  const PagedRun run = few ? paged_run_warp(a, mine, SEG_COST, PARTS_PER_TILE)
-                           : paged_run<THREADS>(a, sm.run, mine, SEG_COST, PARTS_PER_TILE);
+  const PagedRun run = few ? paged_run_warp(a, mine, SEG_COST<G>, PARTS_PER_TILE)
+                           : paged_run<THREADS>(a, sm.run, mine, SEG_COST<G>, PARTS_PER_TILE);
   uint32_t tmem = 0;
   if (warp != 4 && warp != 6) {
-    // the query rows past the box, all weight columns and, for D = 64, the second 64 columns of V (the
-    // upper half of M = 128 dims) are zero: never written by the copies
+    // the query rows past the box and all weight columns are zero (the copies write neither), and so are
+    // the dims past D = 64
     constexpr int NT = THREADS - 64;
     const int tid = warp == 5 ? CT + lane : threadIdx.x;
     uint4* z = reinterpret_cast<uint4*>(&sm.q[0][0]);
@@ -190,11 +198,10 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
       if ((i >> 3) % NQ >= maps.q_rows) z[i] = make_uint4(0u, 0u, 0u, 0u);
     z = reinterpret_cast<uint4*>(&sm.pt[0][0]);
     for (int i = tid; i < (int)sizeof(sm.pt) / 16; i += NT) z[i] = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (DH == 64)
-      for (int st = 0; st < NST; ++st) {
-        z = reinterpret_cast<uint4*>(sm.kv[st][1] + SLAB);
-        for (int i = tid; i < SLAB / 16; i += NT) z[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
+    if constexpr (DH == 64) {
+      z = reinterpret_cast<uint4*>(sm.zero);
+      for (int i = tid; i < SLAB / 16; i += NT) z[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
     fence_proxy_async_smem();
     if (warp == 5) {
       tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
@@ -214,7 +221,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
     const uint64_t pol_kv = l2_policy_evict_first(), pol_q = l2_policy_evict_last();
     const int nslots = kPagedTile >> psn_log2;
-    PagedWalk walk(a, rows, run, SEG_COST);
+    PagedWalk walk(a, rows, run, SEG_COST<G>);
     PagedPiece pc;
     PagedHead hd{};
     int len = 0;
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idS = paged_idesc(NQ, false), idPV = paged_idesc(NP, true);
-      PagedWalk walk(a, rows, run, SEG_COST);
+      PagedWalk walk(a, rows, run, SEG_COST<G>);
       PagedPiece pc;
       uint32_t t = 0, nu = 0;
       bool ok = true;
@@ -308,7 +315,9 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
             !mbar_wait(smem_u32(&sm.o_free[ob]), ((prev_u >> 1) - 1) & 1u, abort_flag, kWaitOFinal, err))
           return false;
         tc_fence_after();
-        const uint64_t vdesc = sw128_desc(smem_u32(sm.kv[s][1]), SLAB, 1024);
+        // the second 64 dims lie one slab further, or in the common zeros
+        const uint32_t v0 = smem_u32(sm.kv[s][1]);
+        const uint64_t vdesc = sw128_desc(v0, DH == 128 ? SLAB : smem_u32(sm.zero) - v0, 1024);
         const uint64_t pdesc = sw128_desc(smem_u32(sm.pt[pb]), 16, 1024);
         const uint32_t tO = tmem + 32 + ob * NP;
 #pragma unroll
@@ -432,7 +441,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
       return true;
     };
 
-    PagedWalk walk(a, rows, run, SEG_COST);
+    PagedWalk walk(a, rows, run, SEG_COST<G>);
     PagedPiece pc;
     uint32_t t = 0, nu = 0;
     PagedPiece nxt;
