@@ -84,7 +84,7 @@ struct PagedSmem {
   alignas(16) typename PagedJoin<pdt::CT, G, DH>::Smem join;
   // mbarriers
   alignas(8) uint64_t k_full[NST], k_empty[NST], v_full[NST], v_empty[NST];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], s_free[2], o_done[2], o_full[2], o_free[2], teardown;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], o_full[2], o_free[2], teardown;
   PagedRunSmem run;
   uint32_t tmem_base;
   int is_last, abort_flag;
@@ -297,75 +297,91 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     }
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idS = paged_idesc(NQ, false), idPV = paged_idesc(NP, true);
-      PagedWalk walk(a, rows, run, SEG_COST<G>);
-      PagedPiece pc;
-      uint32_t t = 0, nu = 0;
-      bool ok = true;
-      bool prev_first = false, prev_last = false;
-      uint32_t prev_u = 0;
-      // O^T += V^T P^T of tile tt
-      auto pv = [&](uint32_t tt) -> bool {
-        const uint32_t s = tt % NST, pb = tt & 1u, ob = prev_u & 1u;
-        if (!mbar_wait(smem_u32(&sm.v_full[s]), (tt / NST) & 1u, abort_flag, kWaitDecodeFull, err) ||
-            !mbar_wait(smem_u32(&sm.p_full[pb]), (tt >> 1) & 1u, abort_flag, kWaitPFull, err))
-          return false;
-        if (prev_first && prev_u >= 2 &&
-            !mbar_wait(smem_u32(&sm.o_free[ob]), ((prev_u >> 1) - 1) & 1u, abort_flag, kWaitOFinal, err))
-          return false;
-        tc_fence_after();
-        // the second 64 dims lie one slab further, or in the common zeros
-        const uint32_t v0 = smem_u32(sm.kv[s][1]);
-        const uint64_t vdesc = sw128_desc(v0, DH == 128 ? SLAB : smem_u32(sm.zero) - v0, 1024);
-        const uint64_t pdesc = sw128_desc(smem_u32(sm.pt[pb]), 16, 1024);
-        const uint32_t tO = tmem + 32 + ob * NP;
+    // The whole warp walks, waits and computes addresses, so that these stay warp-uniform; one elected lane
+    // (the same one every time) issues a product's instructions and the commits that track them.  With one
+    // lane doing everything a tile took 2,150 cycles to issue, more than its bytes take at D = 64.
+    constexpr uint32_t idS = paged_idesc(NQ, false), idPV = paged_idesc(NP, true);
+    constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);    // stride 1024, version 1, 128-byte swizzle
+    auto desc = [](uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4) << 16; };
+    PagedWalk walk(a, rows, run, SEG_COST<G>);
+    PagedPiece pc;
+    uint32_t t = 0, nu = 0;
+    bool ok = true;
+    bool prev_first = false, prev_last = false;
+    uint32_t prev_u = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity, unsigned int site) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, site, err));
+    };
+    // O^T += V^T P^T of tile tt
+    auto pv = [&](uint32_t tt) -> bool {
+      const uint32_t s = tt % NST, pb = tt & 1u, ob = prev_u & 1u;
+      // the softmax had V before it gave its weights
+      if (!wait(&sm.p_full[pb], (tt >> 1) & 1u, kWaitPFull)) return false;
+      if (prev_first && prev_u >= 2 && !wait(&sm.o_free[ob], ((prev_u >> 1) - 1) & 1u, kWaitOFinal)) return false;
+      tc_fence_after();
+      // the second 64 dims lie one slab further, or in the common zeros
+      const uint32_t v0 = smem_u32(sm.kv[s][1]);
+      const uint32_t vd = desc(v0, DH == 128 ? SLAB : smem_u32(sm.zero) - v0), pd = desc(smem_u32(sm.pt[pb]), 16);
+      const uint32_t tO = tmem + 32 + ob * NP;
+      if (elect_one()) {
+        if (prev_first)
+          mma_ss_lo_first(tO, vd, pd, HI, idPV);
+        else
+          mma_ss_lo(tO, vd, pd, HI, idPV);
 #pragma unroll
-        for (int k = 0; k < kPagedTile / 16; ++k)
-          mma_ss(tO, vdesc + ((k * 16 * 128) >> 4), pdesc + ((((k >> 2) * PSLAB) + (k & 3) * 32) >> 4), idPV,
-                 (!prev_first || k > 0) ? 1u : 0u);
+        for (int k = 1; k < kPagedTile / 16; ++k)
+          mma_ss_lo(tO, vd + ((k * 16 * 128) >> 4), pd + (((k >> 2) * PSLAB + (k & 3) * 32) >> 4), HI, idPV);
         mma_commit(smem_u32(&sm.o_done[pb]));
         mma_commit(smem_u32(&sm.v_empty[s]));
         if (prev_last) mma_commit(smem_u32(&sm.o_full[ob]));
-        return true;
-      };
-      PagedPiece nxt;
-      bool more = walk.next(a, rows, nxt);
-      while (ok && more) {
-        pc = nxt;
-        more = walk.next(a, rows, nxt);      // while the piece's first copies are on their way
-        const int qb = nu & 1;
-        if (!mbar_wait(smem_u32(&sm.q_full[qb]), (nu >> 1) & 1u, abort_flag, kWaitQFull, err)) { ok = false; break; }
-        const uint64_t qdesc = sw128_desc(smem_u32(sm.q[qb]), 16, 1024);
-        for (int j = pc.a; j < pc.b && ok; ++j) {
-          const uint32_t s = t % NST, sb = t & 1u;
-          if (!mbar_wait(smem_u32(&sm.k_full[s]), (t / NST) & 1u, abort_flag, kWaitDecodeFull, err) ||
-              (t >= 2 && !mbar_wait(smem_u32(&sm.s_free[sb]), ((t >> 1) - 1) & 1u, abort_flag, kWaitSFull, err))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t kdesc = sw128_desc(smem_u32(sm.kv[s][0]), 16, 1024);
+      }
+      __syncwarp();
+      return true;
+    };
+    PagedPiece nxt;
+    bool more = walk.next(a, rows, nxt);
+    while (ok && more) {
+      pc = nxt;
+      more = walk.next(a, rows, nxt);      // while the piece's first copies are on their way
+      const int qb = nu & 1;
+      if (!wait(&sm.q_full[qb], (nu >> 1) & 1u, kWaitQFull)) {
+        ok = false;
+        break;
+      }
+      const uint32_t qd = desc(smem_u32(sm.q[qb]), 16);
+      for (int j = pc.a; j < pc.b && ok; ++j) {
+        const uint32_t s = t % NST, sb = t & 1u;
+        // the scores' buffer is free: the softmax gave the weights of tile t - 2, which O^T(t - 2) waited for
+        if (!wait(&sm.k_full[s], (t / NST) & 1u, kWaitDecodeFull)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t kd = desc(smem_u32(sm.kv[s][0]), 16), tS = tmem + 16 * sb;
+        if (elect_one()) {
+          mma_ss_lo_first(tS, kd, qd, HI, idS);
 #pragma unroll
-          for (int k = 0; k < DH / 16; ++k)
-            mma_ss(tmem + 16 * sb, kdesc + ((((k >> 2) * SLAB) + (k & 3) * 32) >> 4),
-                   qdesc + ((((k >> 2) * QSLAB) + (k & 3) * 32) >> 4), idS, k > 0 ? 1u : 0u);
+          for (int k = 1; k < DH / 16; ++k)
+            mma_ss_lo(tS, kd + (((k >> 2) * SLAB + (k & 3) * 32) >> 4), qd + (((k >> 2) * QSLAB + (k & 3) * 32) >> 4), HI,
+                      idS);
           mma_commit(smem_u32(&sm.s_full[sb]));
           mma_commit(smem_u32(&sm.k_empty[s]));
           if (j == pc.b - 1) mma_commit(smem_u32(&sm.q_empty[qb]));
-          if (t > 0) ok = pv(t - 1);
-          prev_first = j == pc.a;
-          prev_last = j == pc.b - 1;
-          prev_u = nu;
-          ++t;
         }
-        ++nu;
+        __syncwarp();
+        if (t > 0) ok = pv(t - 1);
+        prev_first = j == pc.a;
+        prev_last = j == pc.b - 1;
+        prev_u = nu;
+        ++t;
       }
-      if (ok && t > 0) pv(t - 1);
-      // every product issued so far must be complete before tensor memory is freed
-      mma_commit(smem_u32(&sm.teardown));
-      mbar_wait(smem_u32(&sm.teardown), 0, nullptr, kWaitTeardown, err);
+      ++nu;
     }
+    if (ok && t > 0) pv(t - 1);
+    // every product issued so far must be complete before tensor memory is freed
+    if (elect_one()) mma_commit(smem_u32(&sm.teardown));
+    __syncwarp();
+    mbar_wait(smem_u32(&sm.teardown), 0, nullptr, kWaitTeardown, err);
   } else {
     // ------------------------------------------------------------ softmax
     const int row = threadIdx.x;                              // key row of S^T, dim of O^T
@@ -456,18 +472,15 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
       }
       for (int j = pc.a; j < pc.b; ++j, ++t) {
         const uint32_t sb = t & 1u, st = t % NST;
-        // the tile's valid counts, the scores, and a weight buffer that O^T has taken
+        // the tile's V and valid counts, and its scores; these were committed after O^T(t - 2), so that
+        // its weight buffer is free as well
         bool good = mbar_wait(smem_u32(&sm.v_full[st]), (t / NST) & 1u, abort_flag, kWaitDecodeFull, err);
         if (good) good = mbar_wait(smem_u32(&sm.s_full[sb]), (t >> 1) & 1u, abort_flag, kWaitSFull, err);
-        if (good && t >= 2)
-          good = mbar_wait(smem_u32(&sm.o_done[sb]), ((t >> 1) - 1) & 1u, abort_flag, kWaitPFull, err);
         __syncwarp();
         tc_fence_after();
         float xs[G];
         paged_tmem_ld<G>(tmem + lane_off + 16 * sb, xs);
         tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(smem_u32(&sm.s_free[sb]));
         const bool valid = in_slot < sm.nvalid[st][slot];
         if (!valid) {
           // neighbouring rows start at different 16-byte columns: 4 rows a wavefront, not 1
