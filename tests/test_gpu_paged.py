@@ -316,6 +316,48 @@ def test_decode_selected_pages(dtype, Hq, Hkv, D, ps, K):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,Hkv", [(20, 3), (90, 3)])
+def test_decode_selected_pages_of_many_sequences(dtype, B, Hkv):
+    # more lists than a warp has lanes, and than a block has threads
+    need_cuda()
+    ps, K, D = 8, 30, 64
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, 500, B)]
+    k, v, tb = make_cache(lens, ps, Hkv, D, dtype, 43)
+    q = queries(B, 2 * Hkv, D, dtype, 44)
+    sel = np.full((B, Hkv, K), -1, dtype=np.int64)
+    n_sel = np.zeros((B, Hkv), dtype=np.int64)
+    for b in range(B):
+        for g in range(Hkv):
+            pick = sorted(rng.permutation(R.cdiv(lens[b], ps))[:rng.integers(0, K + 1)])
+            sel[b, g, :len(pick)] = pick
+            n_sel[b, g] = len(pick)
+    out, lse = ra.ring_attn_decode_paged(q, k, v, tb, ints(lens), sel=ints(sel), n_sel=ints(n_sel))
+    ok()
+    check_decode(out, lse, R.decode(q, k, v, tb, lens, 1 / 8, sel, n_sel), D)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 32, 8), (64, 24, 8), (64, 16, 1)])
+@pytest.mark.parametrize("B", [33, 140])
+def test_decode_batches_of_medium_lengths(D, Hq, Hkv, B):
+    # runs of whole segments and parts of several tiles, more rows than a warp has lanes
+    need_cuda()
+    rng = np.random.default_rng(D + B)
+    lens = [int(x) for x in rng.integers(1, 2500, B)]
+    lens[5], lens[B - 1] = 0, 0
+    k, v, tb = make_cache(lens, 16, Hkv, D, "bf16", 47)
+    q = queries(B, Hq, D, "bf16", 48)
+    ws = ra.decode_paged_workspace(D)
+    out, lse = ra.ring_attn_decode_paged(q, k, v, tb, ints(lens), workspace=ws)
+    ok()
+    check_decode(out, lse, R.decode(q, k, v, tb, lens, 1 / math.sqrt(D)), D)
+    for _ in range(5):
+        o2, l2 = ra.ring_attn_decode_paged(q, k, v, tb, ints(lens), workspace=ws)
+    ok()
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_decode_nan_and_infinite_scores(dtype):
     # a valid NaN key makes its sequence NaN (as the formula does); large scores do not overflow
     need_cuda()
