@@ -85,7 +85,7 @@ struct ScanSmem {
 // `total` pages are numbered through in s.off (those of a sequence that is not
 // served among them).  Up to four a thread, a thread finds its pages' sequences
 // by bisection.  More, a warp takes a sequence's first 128, four sequences'
-// first 32 in flight at once, and the block together the rest of the long ones.
+// 64 in flight at once, and the block together the rest of the long ones.
 // (Extend and trim of 256 sequences with 40 pages: 7.5 us by bisection, 10 the
 // other way; of 1021 sequences with 33,000 pages: 65 and 36 us.)  Called by all
 // threads between barriers.
@@ -103,25 +103,23 @@ __device__ __forceinline__ void move_pages(ScanSmem& s, int n, long long total, 
   }
   if (tid < n && s.count[tid] > OWN) s.long_seq[atomicAdd(&s.n_long, 1)] = tid;
   for (int i0 = warp; i0 < n; i0 += 4 * NW) {
-    int v[4];
+    int count[4], most = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u * NW;
-      v[u] = i < n && lane < s.count[i] ? load(i, lane) : 0;
+      count[u] = i0 + u * NW < n ? min(s.count[i0 + u * NW], OWN) : 0;
+      most = max(most, count[u]);
     }
+    for (int j0 = lane; j0 < most + lane; j0 += 64) {       // the same number of turns in every lane
+      int v[4][2];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u * NW;
-      if (i < n && lane < s.count[i]) store(i, lane, v[u]);
-    }
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u * NW;
-      if (i >= n || s.count[i] <= 32) continue;
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int k = 0; k < 3; ++k) v[k] = lane + 32 * (k + 1) < s.count[i] ? load(i, lane + 32 * (k + 1)) : 0;
+        for (int k = 0; k < 2; ++k) v[u][k] = j0 + 32 * k < count[u] ? load(i0 + u * NW, j0 + 32 * k) : 0;
 #pragma unroll
-      for (int k = 0; k < 3; ++k)
-        if (lane + 32 * (k + 1) < s.count[i]) store(i, lane + 32 * (k + 1), v[k]);
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (j0 + 32 * k < count[u]) store(i0 + u * NW, j0 + 32 * k, v[u][k]);
     }
   }
   __syncthreads();
