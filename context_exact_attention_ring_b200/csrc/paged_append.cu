@@ -6,7 +6,8 @@
 // A copy: bound by memory.  The call's 16-byte pieces (T rows of K and of V)
 // are numbered through and dealt to the threads of blocks of 1024 pieces, four
 // independent loads each before the four stores, so that a single token's row
-// is spread over as many threads as it has pieces and a prompt's over the GPU.
+// is spread over as many threads as it has pieces and a prompt's over the GPU
+// (32k tokens of 8 x 128 bf16: 43 us, 6.2 TB/s read and written).
 #include <cuda_runtime.h>
 
 #include "paged.cuh"

@@ -11,21 +11,21 @@
 // <= 2^-16 p, in columns of their own, and the output is float32-accurate up
 // to its own rounding for the price of the second shared-memory store.
 //
-// Bound by HBM: a tile is 64 KB at D = 128 against 2 x 128 x 16 x D products.
+// Bound by HBM: a tile is 64 KB at D = 128 against 2 x 128 x 16 x D products
+// (6 sequences of 64k to 128k keys, 32/8 heads of 128: 348 us, 6.7 TB/s; 64 ragged
+// ones of 64 to 16,000: 104 us, 6.0 TB/s; one of 77 keys: 6.3 us).
 // One CTA per SM; warp roles:
 //   warps 0-3  softmax: thread t owns tensor-memory lane t (key row t of S^T,
 //              dim t of O^T);
 //   warps 4, 6 producers of K (and Q) and of V: lane i owns page slot i of a
-//              tile (a tile holds 128 / page_size pages, or is part of one)
-//              and looks its page up one tile ahead; each lane issues its
-//              page's TMA boxes into a ring of 3 stages (5 at
-//              D = 64).  Issuing a box takes
-//              60-80 cycles (120 if one lane does it for all), and a tile of
-//              16-token pages is 32 boxes in the 2700 cycles its bytes take:
-//              hence two warps.  The V producer
-//              also leaves each slot's number of valid keys (its stage is
-//              not refilled before the softmax is done with the tile, as K's
-//              is);
+//              tile (a tile holds 128 / page_size pages, or is part of one),
+//              looks its page up one tile ahead and issues its page's TMA
+//              boxes into a ring of stages.  Issuing a box takes 60-80 cycles
+//              (120 if one lane does it for all), and a tile of 16-token
+//              pages is 32 boxes in the 2700 cycles its bytes take: hence two
+//              warps.  The V producer also leaves each slot's number of valid
+//              keys (its stage is not refilled before the softmax is done with
+//              the tile; K's is free as soon as S^T is);
 //   warp 5     MMA issuer and tensor-memory owner.  Tiles follow each other
 //              across segments without a drain: S^T(t+1) is issued before
 //              O^T(t), and Q, O^T and the weights have two buffers.
@@ -53,8 +53,7 @@ constexpr int CT = 128;                     // softmax threads
 constexpr int THREADS = CT + 96;
 constexpr uint32_t TMEM_COLS = 128;         // S^T 2 x 16, O^T 2 x (16 or 32)
 constexpr float LAZY = 8.f;                 // log2 of the growth tolerated before the base moves
-// K/V stages: what shared memory holds.  A V tile stays until its product is done, twice its flight time
-// at D = 64, where three stages of half the bytes reached 0.68 of the copy rate.
+// K/V stages: what shared memory holds (D = 64, 56 sequences of 16,000 keys: 404 us with 3, 395 with 5).
 template <int DH>
 constexpr int NST = DH == 64 ? 5 : 3;
 constexpr int MAX_SLOTS = kPagedTile / 8;   // page slots of a tile

@@ -12,8 +12,9 @@
 // one's V is used, its V during the next scores.  The 8 partial scores of a head
 // are added up across the lanes by halving (4 + 2 + 1 exchanges leave a lane one
 // key), so that a lane takes one maximum and one exponential per head; the
-// weights return through shared memory as pairs.  Bound by instructions, about
-// 85 per head and 8 keys of a group, above two heads, and by memory below.
+// weights return through shared memory as pairs.  Bound by the instructions of a head
+// and 8 keys, and their latencies, above two heads (issue slots 47% busy with
+// 5), and by memory below.
 // (Four keys at a time: 62 us for 400,000 rows of 5 heads of 64, eight: 57, with
 // the runs weighed as now 48.)
 #include <cuda_runtime.h>
