@@ -13,7 +13,7 @@
 // are added up across the lanes by halving (4 + 2 + 1 exchanges leave a lane one
 // key), so that a lane takes one maximum and one exponential per head; the
 // weights return through shared memory as pairs.  Bound by the instructions of a head
-// and 8 keys, and their latencies, above two heads (issue slots 47% busy with
+// and 8 keys, and their latencies, above two heads (issue slots 44% busy with
 // 5), and by memory below.
 // (Four keys at a time: 62 us for 400,000 rows of 5 heads of 64, eight: 57, with
 // the runs weighed as now 48.)
