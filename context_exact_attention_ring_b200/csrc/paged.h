@@ -120,7 +120,7 @@ struct PagedDecodeArgs {
   unsigned int* err;
 };
 size_t paged_decode_workspace_bytes(int D);
-void paged_decode_workspace_split(void* ws, int D, float** part, unsigned int** count);
+void paged_decode_workspace_split(void* ws, float** part, unsigned int** count);
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t st);        // bf16, tensor cores
 cudaError_t launch_paged_decode_simt(const PagedDecodeArgs& a, cudaStream_t st);   // float32, CUDA cores
 

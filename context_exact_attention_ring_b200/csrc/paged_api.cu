@@ -163,7 +163,7 @@ ring_status ring_attn_decode_paged(const void* q, const void* k_pool, const void
     return RING_EINVAL;
   a.q = q; a.k = k_pool; a.v = v_pool; a.table = block_table; a.seq_lens = seq_lens; a.sel = sel; a.n_sel = n_sel;
   a.out = out; a.out_lse = out_lse;
-  paged_decode_workspace_split(workspace, D, &a.ws_part, &a.ws_count);
+  paged_decode_workspace_split(workspace, &a.ws_part, &a.ws_count);
   a.q_b = (long long)q_stride_b;
   a.q_h = (long long)q_stride_h;
   a.table_stride = (long long)table_stride;

@@ -273,15 +273,15 @@ cudaError_t launch_paged_decode_simt(const PagedDecodeArgs& args, cudaStream_t s
   }
 }
 
-static size_t part_bytes(int D) {
-  return ((size_t)2 * kPagedMaxCtas * kPagedHeads * (D + 1) * sizeof(float) + 255) & ~size_t(255);
-}
+// Workspace: the counters first, so that they stay in place (and zero) when calls of either head dimension
+// use one workspace in turn, then the parts.
+static constexpr size_t kCountBytes = (kPagedMaxCtas * sizeof(unsigned int) + 255) & ~size_t(255);
 size_t paged_decode_workspace_bytes(int D) {
-  return part_bytes(D) + ((kPagedMaxCtas * sizeof(unsigned int) + 255) & ~size_t(255));
+  return kCountBytes + (((size_t)2 * kPagedMaxCtas * kPagedHeads * (D + 1) * sizeof(float) + 255) & ~size_t(255));
 }
-void paged_decode_workspace_split(void* ws, int D, float** part, unsigned int** count) {
-  *part = static_cast<float*>(ws);
-  *count = reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(ws) + part_bytes(D));
+void paged_decode_workspace_split(void* ws, float** part, unsigned int** count) {
+  *count = static_cast<unsigned int*>(ws);
+  *part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCountBytes);
 }
 
 }  // namespace ra

@@ -525,7 +525,9 @@ size_t ring_attn_decode_paged_workspace_bytes(int D);
  * workspace: ring_attn_decode_paged_workspace_bytes(D) bytes, 256-byte
  * aligned; its counters must be zero before the first call on it and every
  * call that completes leaves them zero (after RING_ETIMEOUT, zero it again).
- * Calls that share a workspace must not overlap on the GPU.
+ * Calls of any sizes, types and head dimensions may use one workspace in turn
+ * (of the bytes for D = 128); calls that share a workspace must not overlap on
+ * the GPU.
  *
  * Returns RING_EINVAL for null/misaligned pointers, sizes < 1, Hq % Hkv != 0,
  * only one of sel / n_sel, bad strides, scale or dtype, a workspace too small

@@ -500,6 +500,23 @@ def test_two_streams_with_a_workspace_each():
         assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
 
 
+def test_one_workspace_serves_calls_of_all_kinds_in_turn():
+    need_cuda()
+    ws = ra.decode_paged_workspace(128)
+    cases = []
+    for i, (dtype, D, Hq, Hkv, lens) in enumerate((("bf16", 128, 8, 2, [5000, 1300]), ("bf16", 64, 16, 1, [9000]),
+                                                   ("fp32", 64, 4, 2, [3000, 7]), ("fp32", 128, 3, 1, [4000]),
+                                                   ("bf16", 64, 2, 2, [700, 800, 0]))):
+        k, v, tb = make_cache(lens, 16, Hkv, D, dtype, 80 + i)
+        q = queries(len(lens), Hq, D, dtype, 81 + i)
+        cases.append((q, k, v, tb, lens, D))
+    for turn in range(3):
+        got = [ra.ring_attn_decode_paged(*c[:4], ints(c[4]), workspace=ws) for c in cases]
+        ok()
+        for (o, l), c in zip(got, cases):
+            check_decode(o, l, R.decode(*c[:4], c[4], 1 / math.sqrt(c[5])), c[5])
+
+
 def test_two_graphs_that_share_a_workspace_follow_the_lengths():
     # captured calls read lengths, tables and lists on the device; replayed in turn on one stream
     need_cuda()
