@@ -592,7 +592,8 @@ def ring_attn_page_extend(seq_lens, new_lens, block_table, free_pages, n_free, p
 
 def ring_attn_page_trim(seq_lens, keep_lens, block_table, free_pages, n_free, page_size):
     """Cut every sequence to keep_lens[b] tokens (0 ends it) and give the pages
-    past its new end back to the free list, in place."""
+    past its new end back to the free list, in place (negative table entries
+    mark absent pages and are not given back)."""
     dev = _one_device(seq_lens, keep_lens, block_table, free_pages, n_free)
     B = seq_lens.numel()
     tp, W, ts = _table(block_table, B)

@@ -15,7 +15,8 @@
 //
 // page_trim shortens sequences and puts the pages past their new ends back,
 // last taken on top, so that extending and trimming by the same tokens leaves
-// the free list as it was.
+// the free list as it was.  A table entry that marks an absent page is not put
+// there.
 #include <cuda_runtime.h>
 
 #include "kernels.h"
@@ -67,8 +68,11 @@ __device__ __forceinline__ int last_at_most(const T* v, int lo, int hi, T x) {
   return lo;
 }
 
+// Whether a table entry can be a page of a pool, whose slots are 32-bit numbers: an absent page is not.
+__device__ __forceinline__ bool is_page(int page, int ps_log2) { return page >= 0 && page <= (0x7fffffff >> ps_log2); }
+
 __device__ __forceinline__ int slot_at(int page, int pos, int ps_log2) {
-  if (page < 0 || page > (0x7fffffff >> ps_log2)) return -1;
+  if (!is_page(page, ps_log2)) return -1;
   return (page << ps_log2) | (pos & ((1 << ps_log2) - 1));
 }
 
@@ -146,6 +150,7 @@ __global__ void __launch_bounds__(pgt::THREADS, 1) page_extend_kernel(ExtendArgs
   const int n_free = min(max(*a.n_free, 0), a.max_free);
   long long tokens = 0, pages = 0, taken = 0;   // of the sequences before this chunk; pages this call takes
   bool full = false;
+  unsigned largest = 0;       // of the pages given out: one that is no page leaves its tokens without slots
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
     const int b = b0 + tid, in_chunk = min(THREADS, a.B - b0);
     const bool in = b < a.B;
@@ -179,7 +184,10 @@ __global__ void __launch_bounds__(pgt::THREADS, 1) page_extend_kernel(ExtendArgs
     taken = max(taken, mine);
     __syncthreads();
     move_pages(s, in_chunk, total, [&](int i, int j) { return __ldg(a.free_pages + (n_free - 1 - (pages + s.off[i] + j))); },
-               [&](int i, int j, int page) { a.table[(size_t)(b0 + i) * a.table_stride + s.from[i] + j] = page; });
+               [&](int i, int j, int page) {
+                 a.table[(size_t)(b0 + i) * a.table_stride + s.from[i] + j] = page;
+                 largest = max(largest, (unsigned)page);
+               });
     if (one_launch) {
 #pragma unroll 4
       for (int t = tid; t < a.max_tokens; t += THREADS) {
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(pgt::THREADS, 1) page_extend_kernel(ExtendArgs
     for (int w = 1; w < NW; ++w) taken = max(taken, s.warp[w]);
     *a.n_free = n_free - (int)taken;
   }
-  if (full) atomicCAS(a.err, 0u, kFaultCapacity);
+  if (full || !is_page((int)largest, a.ps_log2)) atomicCAS(a.err, 0u, kFaultCapacity);
 }
 
 // Slots [first, first + SLOT_THREADS * SLOTS) by each block: a warp finds the
@@ -259,25 +267,38 @@ cudaError_t launch_page_extend(const ExtendArgs& a, cudaStream_t st) {
   return paged_launch(slot_map_kernel, (a.max_tokens - 1) / per + 1, pgt::SLOT_THREADS, 0, st, a);
 }
 
+// Puts the chunk's pages (n sequences, `total` table entries numbered through
+// in s.off) onto the list from `base` up, the last one first, without the
+// entries that are no page.  Returns how many pages there are.
+__device__ __forceinline__ long long trim_present(const TrimArgs& a, ScanSmem& s, int b0, int n, long long total,
+                                               long long base) {
+  using namespace pgt;
+  long long done = 0;
+  for (long long g0 = 0; g0 < total; g0 += THREADS) {
+    const long long g = total - 1 - g0 - threadIdx.x;
+    int page = -1;
+    if (g >= 0) {
+      const int i = last_at_most(s.off, 0, n, g);
+      page = a.table[(size_t)(b0 + i) * a.table_stride + s.from[i] + (g - s.off[i])];
+    }
+    const bool present = is_page(page, a.ps_log2);
+    long long turn;
+    const long long to = base + done + block_scan(present, s.warp, &turn) - 1;
+    if (present && to < a.max_free) a.free_pages[to] = page;
+    done += turn;
+  }
+  return done;
+}
+
+// The last chunk of sequences first: its pages lie lowest on the list.
 __global__ void __launch_bounds__(pgt::THREADS, 1) page_trim_kernel(TrimArgs a) {
   using namespace pgt;
   __shared__ ScanSmem s;
   paged_begin();
   const int tid = threadIdx.x;
   const long long cap = (long long)a.W << a.ps_log2;
-  const int n_free = min(max(*a.n_free, 0), a.max_free);
-  long long all = 0, total;      // pages given back by all sequences
-  if (a.B > THREADS) {
-    for (int b = tid; b < a.B; b += THREADS) {
-      const long long len = min(max((long long)a.seq_lens[b], 0LL), cap);
-      const long long keep = min(max((long long)a.keep_lens[b], 0LL), len);
-      all += pages_of(len, a.ps_log2) - pages_of(keep, a.ps_log2);
-    }
-    block_scan(all, s.warp, &total);
-    all = total;
-  }
-  long long before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+  long long base = min(max(*a.n_free, 0), a.max_free), total;
+  for (int b0 = (a.B - 1) / THREADS * THREADS; b0 >= 0; b0 -= THREADS) {
     const int b = b0 + tid, in_chunk = min(THREADS, a.B - b0);
     long long len = 0, keep = 0;
     if (b < a.B) {
@@ -287,26 +308,30 @@ __global__ void __launch_bounds__(pgt::THREADS, 1) page_trim_kernel(TrimArgs a) 
     const int from = pages_of(keep, a.ps_log2);
     const int gone = pages_of(len, a.ps_log2) - from;
     const long long upto = block_scan(gone, s.warp, &total);
-    if (a.B <= THREADS) all = total;
     s.off[tid] = upto - gone;
     s.from[tid] = from;
     s.count[tid] = gone;
     if (tid == 0) s.n_long = 0;
     if (b < a.B) a.seq_lens[b] = (int)keep;
     __syncthreads();
+    // as if every entry were a page; where one is not (rare), the chunk's pages are placed again
+    unsigned largest = 0;
     move_pages(s, in_chunk, total,
                [&](int i, int j) { return __ldg(a.table + (size_t)(b0 + i) * a.table_stride + s.from[i] + j); },
                [&](int i, int j, int page) {
-                 const long long to = n_free + all - 1 - (before + s.off[i] + j);
+                 const long long to = base + total - 1 - (s.off[i] + j);
                  if (to < a.max_free) a.free_pages[to] = page;     // the list cannot hold more
+                 largest = max(largest, (unsigned)page);
                });
-    before += total;
-    __syncthreads();    // s is free
+    if (__syncthreads_or(!is_page((int)largest, a.ps_log2))) {
+      total = trim_present(a, s, b0, in_chunk, total, base);
+      __syncthreads();
+    }
+    base += total;      // s is free
   }
   if (tid == 0) {
-    const long long room = min(all, (long long)a.max_free - n_free);
-    *a.n_free = n_free + (int)room;
-    if (room < all) atomicCAS(a.err, 0u, kFaultCapacity);
+    *a.n_free = (int)min(base, (long long)a.max_free);
+    if (base > a.max_free) atomicCAS(a.err, 0u, kFaultCapacity);
   }
 }
 

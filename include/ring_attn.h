@@ -444,15 +444,18 @@ ring_status ring_attn_kv_append(void* k_cache, void* v_cache, const void* k_new,
  *                     are numbered cu_new[b] .. cu_new[b+1]-1 in sequence b
  *   start_lens [B]    the length before the call, or -1 (see below)
  *   slot_map [max_tokens]  token t's cache row, page*page_size + offset; -1
- *                     for the numbers from cu_new[B] on and for the tokens of
- *                     a sequence that was left as it was
+ *                     for the numbers from cu_new[B] on, for the tokens of a
+ *                     sequence that was left as it was, and for tokens whose
+ *                     page is marked absent
  *   seq_lens, n_free  advanced.
  * A sequence is left as it was (start_lens -1) if its new length exceeds
  * W*page_size, if its tokens pass max_tokens, or if the free list does not
  * hold its pages after those of the sequences before it (a sequence that
  * needs no new page, or gets no token, is served all the same);
- * ring_attn_device_error() then reports RING_ECAPACITY.  Entries of block_table that are not taken into use
- * keep their value.  The page numbers themselves are not checked here.
+ * ring_attn_device_error() then reports RING_ECAPACITY.  It does so, too,
+ * where the list gives out an entry that can be no pool's page (negative, or
+ * its rows beyond 2^31); otherwise the list's page numbers are not checked.
+ * Entries of block_table that are not taken into use keep their value.
  * Returns RING_EINVAL for null/misaligned pointers, sizes < 1, table_stride <
  * W or W*page_size beyond 32 bits; RING_EUNSUPPORTED for a page size that is
  * not built; RING_ECUDA on launch failure.
@@ -470,10 +473,14 @@ ring_status ring_attn_page_extend(int32_t* seq_lens, const int32_t* new_lens, in
  * ends the sequence, seq_lens[b] leaves it).  The pages past the new ends go
  * onto the free list, the last of the last sequence first, so that extending
  * by some tokens and cutting the same tokens off again restores the list.
- * free_pages has room for max_free pages; what would pass that is dropped and
- * ring_attn_device_error() reports RING_ECAPACITY.  block_table is not
- * changed.  A page in two sequences' tables is given back once for each: where
- * sequences share pages, the caller keeps count.
+ * An entry of block_table that can be no pool's page (negative, or its rows
+ * beyond 2^31) marks an absent page and is not given back; any other entry is
+ * taken for a page, since the call does not know the pool: where sequences
+ * are trimmed, absent pages are marked by -1.  free_pages has room for
+ * max_free pages (its entries from n_free[0] on are scratch); what would pass
+ * that is dropped and ring_attn_device_error() reports RING_ECAPACITY.
+ * block_table is not changed.  A page in two sequences' tables is given back
+ * once for each: where sequences share pages, the caller keeps count.
  * Errors as ring_attn_page_extend.
  * The source pages have no counterpart.
  */

@@ -1,0 +1,89 @@
+"""GPU tests of the paged-cache operators where their inputs mark something as
+missing: absent pages, sequences that were not served, full lists, infinities."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import context_exact_attention_ring_b200 as ra
+from tests import paged_ref as R
+from tests.helpers import need_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Present(R.Tables):
+    """The reference tables, whose trim gives no absent page back."""
+
+    def trim(self, keep):
+        ps, back = self.ps, []
+        for b, kp in enumerate(keep):
+            old = min(max(self.lens[b], 0), self.table.shape[1] * ps)
+            kp = min(max(int(kp), 0), old)
+            pages = [int(x) for x in self.table[b, R.cdiv(kp, ps):R.cdiv(old, ps)]]
+            back += [p for p in pages if 0 <= p <= (2 ** 31 - 1) // ps]
+            self.lens[b] = kp
+        back, room = back[::-1], len(self.free) - self.n
+        for p in back[:room]:
+            self.free[self.n] = p
+            self.n += 1
+        return len(back) > room
+
+
+@pytest.mark.parametrize("B,hi,room,ps", [(1, 90, 400, 16), (7, 400, 300, 8), (300, 400, 9000, 16), (300, 400, None, 16),
+                                          (2500, 400, 70000, 16), (2500, 400, 20000, 16), (9, 20000, 12000, 16),
+                                          (9, 20000, None, 16), (6, 20000, 3000, 32)])
+def test_trim_gives_no_absent_page_back(B, hi, room, ps):
+    # few pages (one a thread) and many (a warp to a sequence, the block together), several chunks of sequences, a
+    # list that has room for the pages only without the absent ones, or not even then
+    need_cuda()
+    rng = np.random.default_rng(B + (room or 0))
+    W = R.cdiv(hi, ps) + 50
+    lens = [int(x) for x in rng.integers(1, hi, B)]
+    need = [R.cdiv(n, ps) for n in lens]
+    perm = rng.permutation(sum(need) + 300)
+    table, at = np.full((B, W), -9, dtype=np.int64), 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        gone = rng.random(n) < (0.3 if b % 3 else 0.0)
+        table[b, :n][gone] = rng.choice([-1, -2 ** 31, 2 ** 31 - 1], int(gone.sum()))
+        at += n
+    if B == 1:
+        table[0, 1] = -1
+    free = list(perm[at:])
+    keep = [0 if b % 2 == 0 else n // 2 for b, n in enumerate(lens)]
+    if room is None:                                     # as many as come back
+        fit = Present(lens, table, free + [0] * sum(need), len(free), ps)
+        fit.trim(keep)
+        room = fit.n
+    ref = Present(lens, table, (free + [0] * room)[:room], min(len(free), room), ps)
+    sl, tb, fr, nf = ints(lens), ints(table), ints(ref.free), ints([ref.n])
+    ra.ring_attn_page_trim(sl, ints(keep), tb, fr, nf, ps)
+    over = ref.trim(keep)
+    torch.cuda.synchronize()
+    assert ra.ring_attn_device_error()[0] == (ra.RING_ECAPACITY if over else ra.RING_OK)
+    assert sl.tolist() == ref.lens and nf.tolist() == [ref.n] and fr[:ref.n].tolist() == ref.free[:ref.n]
+    # another sequence gets pages, all of them
+    news = [0] * B
+    news[0] = min(ref.n, 40) * ps
+    slots, start, cu = ra.ring_attn_page_extend(sl, ints(news), tb, fr, nf, ps, max_tokens=sum(news))
+    want = ref.extend(news, sum(news))
+    torch.cuda.synchronize()
+    assert ra.ring_attn_device_error()[0] == ra.RING_OK
+    assert slots.tolist() == want[0] and min(want[0]) >= 0 and start.tolist() == want[1] and nf.tolist() == [ref.n]
+
+
+def test_extend_reports_a_list_entry_that_is_no_page():
+    need_cuda()
+    for bad in (-1, 2 ** 31 - 1):
+        sl, tb, nf = ints([0, 3]), ints([[-5] * 3, [4, -5, -5]]), ints([3])
+        slots, start, cu = ra.ring_attn_page_extend(sl, ints([20, 5]), tb, ints([7, bad, 2]), nf, 16, max_tokens=25)
+        torch.cuda.synchronize()
+        assert ra.ring_attn_device_error()[0] == ra.RING_ECAPACITY
+        assert slots.tolist() == [2 * 16 + i for i in range(16)] + [-1] * 4 + [4 * 16 + i for i in range(3, 8)]
+        assert tb.tolist() == [[2, bad, -5], [4, -5, -5]] and nf.tolist() == [1] and sl.tolist() == [20, 8]
