@@ -97,6 +97,10 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st);
 constexpr int kPagedMaxCtas = 148;
 constexpr int kPagedTile = 128;       // keys per tile, the unit the work is split in
 constexpr int kPagedHeads = 16;       // query heads a CTA works on at once (a head group)
+constexpr int kPagedSimtHeads = 8;    // the same of the float32 kernel
+// What a segment costs besides its tiles, in tiles, of G query heads per kv head (measured: see the kernels).
+__host__ __device__ constexpr int paged_seg_cost(int G) { return G > 8 ? 2 : 1; }
+constexpr int kPagedSimtSegCost = 2;
 
 struct PagedDecodeArgs {
   const void* q;                // [B, Hq, D], strides q_b, q_h

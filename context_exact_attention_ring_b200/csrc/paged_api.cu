@@ -154,11 +154,13 @@ ring_status ring_attn_decode_paged(const void* q, const void* k_pool, const void
   const int eb = elem_bytes(dtype);
   if (!good_rows(q_stride_b, q_stride_h, B, Hq, D, eb)) return RING_EINVAL;
   if (!table_fits(W, pl) || table_stride >= (size_t(1) << 32) || (sel && !table_fits(K, pl))) return RING_EINVAL;
-  // units of the call (tiles, and one per segment: a kv head's group of at most 8 query heads or more) count in 32 bits
+  // outputs, and the call's units (per segment its tiles and its fixed cost), count in 32 bits
+  if ((long long)B * Hq > 0x7fffffffLL / D) return RING_EINVAL;
   const long long keys = (long long)(sel ? K : W) << pl;
-  const long long segs = (long long)B * Hkv * ((Hq / Hkv + 7) / 8);
-  if (segs * ((keys + kPagedTile - 1) / kPagedTile + 1) > 0x7fffffffLL || (long long)B * Hq * D > 0x7fffffffLL)
-    return RING_EINVAL;
+  const int G = Hq / Hkv, group = dtype == RING_BF16 ? kPagedHeads : kPagedSimtHeads;
+  const int seg_cost = dtype == RING_BF16 ? paged_seg_cost(G) : kPagedSimtSegCost;
+  const long long segs = (long long)B * Hkv * ((G + group - 1) / group);
+  if (segs * ((keys + kPagedTile - 1) / kPagedTile + seg_cost) > 0x7fffffffLL) return RING_EINVAL;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < paged_decode_workspace_bytes(D))
     return RING_EINVAL;
   a.q = q; a.k = k_pool; a.v = v_pool; a.table = block_table; a.seq_lens = seq_lens; a.sel = sel; a.n_sel = n_sel;
@@ -168,7 +170,7 @@ ring_status ring_attn_decode_paged(const void* q, const void* k_pool, const void
   a.q_h = (long long)q_stride_h;
   a.table_stride = (long long)table_stride;
   a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.num_pages = num_pages; a.ps_log2 = pl; a.W = W; a.K = sel ? K : 0;
-  a.G = Hq / Hkv;
+  a.G = G;
   a.scale = scale;
   a.out_fp32 = out_dtype == RING_FP32;
   a.err = error_word();

@@ -61,7 +61,7 @@ constexpr int MAX_SLOTS = kPagedTile / 8;   // page slots of a tile
 // heads (64 ragged sequences with 16 heads to a kv head: 129 us with 1, 111 with 2; with 4 heads 103 and 103,
 // 128 shorter ones 54 and 57).
 template <int G>
-constexpr int SEG_COST = G > 8 ? 2 : 1;
+constexpr int SEG_COST = paged_seg_cost(G);
 constexpr int PARTS_PER_TILE = 20;          // parts joined in the time of a tile
 }  // namespace pdt
 

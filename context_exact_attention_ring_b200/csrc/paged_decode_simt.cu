@@ -28,10 +28,10 @@ namespace ra {
 namespace pds {
 constexpr int THREADS = 512;
 constexpr int NW = THREADS / 32;
-constexpr int HEADS = 8;               // query heads of a group, at most
+constexpr int HEADS = kPagedSimtHeads;  // query heads of a group, at most
 // What a segment costs besides its tiles (queries, the empty pipeline, the warps' sums), in tiles; with 1
 // the case of 5 heads took 57 us, with 2 and 3 it takes 48.
-constexpr int SEG_COST = 2;
+constexpr int SEG_COST = kPagedSimtSegCost;
 constexpr int PARTS_PER_TILE = 20;     // parts joined in the time of a tile
 }  // namespace pds
 

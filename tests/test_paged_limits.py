@@ -1,0 +1,25 @@
+"""Sizes of the paged-cache calls at the edge of 32-bit counts: what passes it is
+refused on the host (every case fails before a launch)."""
+import pytest
+
+import context_exact_attention_ring_b200 as ra
+from tests.test_paged_refusals import DECODE, E, built, call    # noqa: F401 (built: fixture)
+
+BIG = dict(N=1 << 20, sp=1 << 16)
+
+
+@pytest.mark.parametrize("kw", [
+    # a segment is a kv head's group of 8 query heads (float32) or 16 (bf16), and counts its tiles of 128 keys and its
+    # fixed cost: 2 (float32, bf16 above 8 heads) or 1; 2^31 of them are one too many
+    dict(dtype=1, out_dtype=1, B=1 << 20, Hq=1, Hkv=1, ps=128, W=2046, ts=2046),
+    dict(dtype=1, out_dtype=1, B=1 << 14, Hq=64 * 16, Hkv=64, ps=128, W=1022, ts=1022, qb=1 << 16),
+    dict(dtype=1, out_dtype=1, B=33554431, Hq=1, Hkv=1, ps=128, W=63, ts=63),
+    dict(dtype=1, out_dtype=1, B=1 << 20, Hq=1, Hkv=1, ps=128, W=8, ts=8, sel=1 << 16, n_sel=1 << 16, K=2046),
+    dict(B=1 << 20, Hq=1, Hkv=1, ps=128, W=2047, ts=2047),
+    dict(B=1 << 16, Hq=16 * 16, Hkv=16, ps=128, W=2046, ts=2046, qb=1 << 16),
+    # products of sizes that pass 64 bits
+    dict(B=1 << 30, Hq=1 << 30, Hkv=1, W=1, ts=1, qb=1 << 35), dict(B=1 << 30, Hq=1 << 30, Hkv=1 << 30, W=1, ts=1, qb=1 << 35),
+    dict(B=(1 << 31) - 1, Hq=(1 << 31) - 1, Hkv=(1 << 31) - 1, ps=128, W=1 << 20, ts=1 << 20, qb=1 << 35),
+])
+def test_decode_units_are_counted_with_their_kernels_cost(kw):
+    assert call("ring_attn_decode_paged", {**DECODE, **BIG}, **kw) == E
