@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(pgt::SLOT_THREADS) slot_map_kernel(ExtendArgs 
   paged_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int first = blockIdx.x * (SLOT_THREADS * SLOTS);
-  const int last = min(first + SLOT_THREADS * SLOTS, a.max_tokens) - 1;
+  const int last = min(first + (SLOT_THREADS * SLOTS - 1), a.max_tokens - 1);    // below 2^31 whatever max_tokens
   const int all = a.cu_new[a.B];
   if (warp < 2) {
     const int t = min(warp ? last : first, max(all - 1, 0));

@@ -87,3 +87,19 @@ def test_extend_reports_a_list_entry_that_is_no_page():
         assert ra.ring_attn_device_error()[0] == ra.RING_ECAPACITY
         assert slots.tolist() == [2 * 16 + i for i in range(16)] + [-1] * 4 + [4 * 16 + i for i in range(3, 8)]
         assert tb.tolist() == [[2, bad, -5], [4, -5, -5]] and nf.tolist() == [1] and sl.tolist() == [20, 8]
+
+
+def test_slot_map_of_2_to_the_31_entries():
+    # the last block's entries end where 32-bit numbers do (8.6 GB)
+    need_cuda()
+    T, ps = 2 ** 31 - 1, 1024
+    slot_map = torch.full((T,), 7, device="cuda", dtype=torch.int32)
+    lens, news = [0] * 70, [3] * 70
+    tb, free = ints([[-1]] * 70), ints(list(range(100)))
+    slots, start, cu = ra.ring_attn_page_extend(ints(lens), ints(news), tb, free, ints([100]), ps, slot_map=slot_map)
+    torch.cuda.synchronize()
+    assert ra.ring_attn_device_error()[0] == ra.RING_OK
+    assert slots[:210].tolist() == [(99 - t // 3) * ps + t % 3 for t in range(210)]
+    for at in range(210, T, 1 << 28):
+        part = slots[at:at + (1 << 28)]
+        assert int(part.min()) == int(part.max()) == -1, at
