@@ -51,6 +51,7 @@ struct PoolStrides {
 };
 
 // ---- block tables and slot maps ----
+constexpr int kPagedMaxSeqs = 0x7fffffff - 1024;   // sequences are counted in 32 bits, past the last of them by a block
 struct ExtendArgs {
   int32_t* seq_lens;          // [B], advanced
   const int32_t* new_lens;    // [B]

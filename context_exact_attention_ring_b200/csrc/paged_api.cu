@@ -74,7 +74,7 @@ ring_status ring_attn_page_extend(int32_t* seq_lens, const int32_t* new_lens, in
   if (B < 1 || W < 1 || max_free < 1 || max_tokens < 1 || page_size < 1 || table_stride < (size_t)W) return RING_EINVAL;
   const int pl = page_log2(page_size);
   if (pl < 0) return RING_EUNSUPPORTED;
-  if (!table_fits(W, pl) || table_stride >= (size_t(1) << 32)) return RING_EINVAL;
+  if (B > kPagedMaxSeqs || !table_fits(W, pl) || table_stride >= (size_t(1) << 32)) return RING_EINVAL;
   ExtendArgs a{};
   a.seq_lens = seq_lens; a.new_lens = new_lens; a.table = block_table; a.free_pages = free_pages; a.n_free = n_free;
   a.slot_map = slot_map; a.start_lens = start_lens; a.cu_new = cu_new;
@@ -93,7 +93,7 @@ ring_status ring_attn_page_trim(int32_t* seq_lens, const int32_t* keep_lens, con
   if (B < 1 || W < 1 || max_free < 1 || page_size < 1 || table_stride < (size_t)W) return RING_EINVAL;
   const int pl = page_log2(page_size);
   if (pl < 0) return RING_EUNSUPPORTED;
-  if (!table_fits(W, pl) || table_stride >= (size_t(1) << 32)) return RING_EINVAL;
+  if (B > kPagedMaxSeqs || !table_fits(W, pl) || table_stride >= (size_t(1) << 32)) return RING_EINVAL;
   TrimArgs a{};
   a.seq_lens = seq_lens; a.keep_lens = keep_lens; a.table = block_table; a.free_pages = free_pages; a.n_free = n_free;
   a.table_stride = (long long)table_stride;

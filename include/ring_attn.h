@@ -457,8 +457,8 @@ ring_status ring_attn_kv_append(void* k_cache, void* v_cache, const void* k_new,
  * its rows beyond 2^31); otherwise the list's page numbers are not checked.
  * Entries of block_table that are not taken into use keep their value.
  * Returns RING_EINVAL for null/misaligned pointers, sizes < 1, table_stride <
- * W or W*page_size beyond 32 bits; RING_EUNSUPPORTED for a page size that is
- * not built; RING_ECUDA on launch failure.
+ * W, W*page_size beyond 32 bits or B above 2^31 - 1025; RING_EUNSUPPORTED for a
+ * page size that is not built; RING_ECUDA on launch failure.
  * The source pages have no counterpart.
  */
 ring_status ring_attn_page_extend(int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table,

@@ -3,7 +3,7 @@ refused on the host (every case fails before a launch)."""
 import pytest
 
 import context_exact_attention_ring_b200 as ra
-from tests.test_paged_refusals import DECODE, E, built, call    # noqa: F401 (built: fixture)
+from tests.test_paged_refusals import (BOUNDS, DECODE, EXTEND, SELECT, TRIM, E, built, call)  # noqa: F401 (built: fixture)
 
 BIG = dict(N=1 << 20, sp=1 << 16)
 
@@ -23,3 +23,13 @@ BIG = dict(N=1 << 20, sp=1 << 16)
 ])
 def test_decode_units_are_counted_with_their_kernels_cost(kw):
     assert call("ring_attn_decode_paged", {**DECODE, **BIG}, **kw) == E
+
+
+TOP = (1 << 31) - 1
+
+
+@pytest.mark.parametrize("B", [TOP, TOP - 1022])
+def test_sequence_counts_that_the_scan_would_step_past(B):
+    # the block that scans takes 1024 sequences at a time, the last step's end included
+    assert call("ring_attn_page_extend", EXTEND, B=B) == E
+    assert call("ring_attn_page_trim", TRIM, B=B) == E
