@@ -231,7 +231,7 @@ ring_status ring_attn_page_select(const float* scores, const int32_t* seq_lens, 
     return RING_EINVAL;
   const int pl = page_log2(page_size);
   if (pl < 0) return RING_EUNSUPPORTED;
-  if (!table_fits(W, pl) || (long long)B * Hkv > 0x7fffffffLL) return RING_EINVAL;
+  if (!table_fits(W, pl) || !table_fits(K, pl) || (long long)B * Hkv > 0x7fffffffLL) return RING_EINVAL;
   SelectArgs a{scores, seq_lens, sel, n_sel, B, Hkv, W, pl, K, keep_first, keep_last};
   return from_cuda(launch_page_select(a, reinterpret_cast<cudaStream_t>(stream)));
 }

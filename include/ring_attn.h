@@ -597,8 +597,9 @@ ring_status ring_attn_page_scores(const void* q, const void* bounds, const int32
  * ascending order, then -1; n_sel [B,Hkv] their number: the lists of
  * ring_attn_decode_paged.
  * Returns RING_EINVAL for null/misaligned pointers, sizes < 1, keep_first or
- * keep_last < 0 or together above K; RING_EUNSUPPORTED for a page size that is
- * not built; RING_ECUDA on launch failure.
+ * keep_last < 0 or together above K, W*page_size, K*page_size or B*Hkv beyond
+ * 32 bits; RING_EUNSUPPORTED for a page size that is not built; RING_ECUDA on
+ * launch failure.
  * The source pages have no counterpart.
  */
 ring_status ring_attn_page_select(const float* scores, const int32_t* seq_lens, int32_t* sel, int32_t* n_sel, int B,

@@ -33,3 +33,9 @@ def test_sequence_counts_that_the_scan_would_step_past(B):
     # the block that scans takes 1024 sequences at a time, the last step's end included
     assert call("ring_attn_page_extend", EXTEND, B=B) == E
     assert call("ring_attn_page_trim", TRIM, B=B) == E
+
+
+@pytest.mark.parametrize("kw", [dict(K=TOP), dict(K=TOP - 1000, ps=8), dict(K=1 << 28, ps=8), dict(K=1 << 27, ps=16)])
+def test_select_lists_longer_than_any_sequence(kw):
+    # as for the decode that reads them: K pages hold fewer than 2^31 tokens
+    assert call("ring_attn_page_select", SELECT, **kw) == E
