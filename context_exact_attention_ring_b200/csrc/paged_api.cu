@@ -192,6 +192,7 @@ ring_status ring_attn_page_bounds(const void* k_pool, void* bounds, const int32_
                                     &a.pool);
   if (rs != RING_OK) return rs;
   if (!table_fits(W, pl) || table_stride >= (size_t(1) << 32)) return RING_EINVAL;
+  if ((long long)Hkv * D > 0x7fffffffLL / elem_bytes(dtype)) return RING_EINVAL;    // bytes of a token's row
   a.k = k_pool; a.bounds = bounds; a.table = block_table; a.seq_lens = seq_lens; a.start_lens = start_lens;
   a.table_stride = (long long)table_stride;
   a.B = B; a.Hkv = Hkv; a.D = D; a.num_pages = num_pages; a.ps_log2 = pl; a.W = W; a.elem_bytes = elem_bytes(dtype);

@@ -39,3 +39,9 @@ def test_sequence_counts_that_the_scan_would_step_past(B):
 def test_select_lists_longer_than_any_sequence(kw):
     # as for the decode that reads them: K pages hold fewer than 2^31 tokens
     assert call("ring_attn_page_select", SELECT, **kw) == E
+
+
+@pytest.mark.parametrize("kw", [dict(Hkv=1 << 26, D=128), dict(Hkv=1 << 25, D=64), dict(Hkv=1 << 25, D=128, dtype=1),
+                                dict(Hkv=TOP, D=64, dtype=1)])
+def test_bounds_of_rows_beyond_32_bits(kw):
+    assert call("ring_attn_page_bounds", BOUNDS, B=1, **kw) == E
