@@ -512,7 +512,10 @@ def _launch(name, dev, *args):
     """Call the library on the tensors' device, on that device's current torch stream."""
     call, words, n = _PACKED[name]
     fn = (_lib or lib()).ring_attn_paged_packed
-    packed = words.pack(*args)
+    try:
+        packed = words.pack(*args)
+    except struct.error:
+        raise ValueError(f"{name}: an argument is no 64-bit integer") from None
     if torch.cuda.current_device() == dev:
         st = fn(call, packed, n, _raw_stream(dev))
     else:

@@ -239,6 +239,14 @@ ring_status ring_attn_page_select(const float* scores, const int32_t* seq_lens, 
 
 ring_status ring_attn_paged_packed(int call, const int64_t* args, int n, void* stream) {
   if (!args || (reinterpret_cast<uintptr_t>(args) & 7u)) return RING_EINVAL;
+  // per call, in order: how many words, and which of them are ints (bit i: word i), which may not be cut
+  static constexpr struct {
+    int n;
+    uint32_t ints;
+  } kWords[] = {{14, 0x3b00u}, {10, 0x360u}, {16, 0x83e0u}, {28, 0x301fe00u}, {16, 0x87e0u}, {16, 0x8fe0u}, {11, 0x7f0u}};
+  if (call < 0 || call > RING_PAGE_SELECT || n != kWords[call].n) return RING_EINVAL;
+  for (int i = 0; i < n; ++i)
+    if ((kWords[call].ints >> i & 1u) && args[i] != static_cast<int>(args[i])) return RING_EINVAL;
   // the arguments in order: pointers, ints and sizes as they are, the scale as the bits of a double
   auto ptr = [&](int i) { return reinterpret_cast<void*>(static_cast<intptr_t>(args[i])); };
   auto i32 = [&](int i) { return reinterpret_cast<int32_t*>(ptr(i)); };
@@ -247,19 +255,15 @@ ring_status ring_attn_paged_packed(int call, const int64_t* args, int n, void* s
   auto size = [&](int i) { return static_cast<size_t>(args[i]); };
   switch (call) {
     case RING_PAGE_EXTEND:
-      if (n != 14) return RING_EINVAL;
       return ring_attn_page_extend(i32(0), i32(1), i32(2), i32(3), i32(4), i32(5), i32(6), i32(7), num(8), num(9),
                                    size(10), num(11), num(12), num(13), stream);
     case RING_PAGE_TRIM:
-      if (n != 10) return RING_EINVAL;
       return ring_attn_page_trim(i32(0), i32(1), i32(2), i32(3), i32(4), num(5), num(6), size(7), num(8), num(9),
                                  stream);
     case RING_PAGED_APPEND:
-      if (n != 16) return RING_EINVAL;
       return ring_attn_paged_append(ptr(0), ptr(1), ptr(2), ptr(3), i32(4), num(5), num(6), num(7), num(8), num(9),
                                     size(10), size(11), size(12), size(13), size(14), num(15), stream);
     case RING_DECODE_PAGED: {
-      if (n != 28) return RING_EINVAL;
       double scale;
       memcpy(&scale, args + 23, sizeof(scale));
       return ring_attn_decode_paged(ptr(0), ptr(1), ptr(2), i32(3), i32(4), i32(5), i32(6), ptr(7), f32(8), num(9),
@@ -268,15 +272,12 @@ ring_status ring_attn_paged_packed(int call, const int64_t* args, int n, void* s
                                     ptr(26), size(27), stream);
     }
     case RING_PAGE_BOUNDS:
-      if (n != 16) return RING_EINVAL;
       return ring_attn_page_bounds(ptr(0), ptr(1), i32(2), i32(3), i32(4), num(5), num(6), num(7), num(8), num(9),
                                    num(10), size(11), size(12), size(13), size(14), num(15), stream);
     case RING_PAGE_SCORES:
-      if (n != 16) return RING_EINVAL;
       return ring_attn_page_scores(ptr(0), ptr(1), i32(2), i32(3), f32(4), num(5), num(6), num(7), num(8), num(9),
                                    num(10), num(11), size(12), size(13), size(14), num(15), stream);
     case RING_PAGE_SELECT:
-      if (n != 11) return RING_EINVAL;
       return ring_attn_page_select(f32(0), i32(1), i32(2), i32(3), num(4), num(5), num(6), num(7), num(8), num(9),
                                    num(10), stream);
   }

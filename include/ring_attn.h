@@ -618,7 +618,8 @@ typedef enum {
  * argument (ctypes takes 2.4 us for ring_attn_decode_paged's, 1.1 us packed).
  * args is host memory, read before the call returns.
  * Returns what the call returns; RING_EINVAL for an unknown call, a null or
- * misaligned args, or another number of words than the call has arguments.
+ * misaligned args, another number of words than the call has arguments, or a
+ * word for an int that is none.
  * The source pages have no counterpart.
  */
 ring_status ring_attn_paged_packed(int call, const int64_t* args, int n, void* stream);

@@ -3,7 +3,8 @@ refused on the host (every case fails before a launch)."""
 import pytest
 
 import context_exact_attention_ring_b200 as ra
-from tests.test_paged_refusals import (BOUNDS, DECODE, EXTEND, SELECT, TRIM, E, built, call)  # noqa: F401 (built: fixture)
+from tests.test_paged_refusals import (APPEND, BOUNDS, DECODE, EXTEND, SCORES, SELECT, TRIM, E, built,  # noqa: F401
+                                        call)    # built: fixture
 
 BIG = dict(N=1 << 20, sp=1 << 16)
 
@@ -45,3 +46,30 @@ def test_select_lists_longer_than_any_sequence(kw):
                                 dict(Hkv=TOP, D=64, dtype=1)])
 def test_bounds_of_rows_beyond_32_bits(kw):
     assert call("ring_attn_page_bounds", BOUNDS, B=1, **kw) == E
+
+
+PACKED_INTS = {
+    "ring_attn_page_extend": (EXTEND, "B W ps max_free max_tokens"),
+    "ring_attn_page_trim": (TRIM, "B W ps max_free"),
+    "ring_attn_paged_append": (APPEND, "T Hkv D N ps dtype"),
+    "ring_attn_decode_paged": (DECODE, "B Hq Hkv D N ps W K dtype out_dtype"),
+    "ring_attn_page_bounds": (BOUNDS, "B Hkv D N ps W dtype"),
+    "ring_attn_page_scores": (SCORES, "B Hq Hkv D N ps W dtype"),
+    "ring_attn_page_select": (SELECT, "B Hkv W ps K first last"),
+}
+
+
+@pytest.mark.parametrize("name", sorted(PACKED_INTS))
+def test_packed_integers_are_not_cut_to_32_bits(name):
+    base, ints = PACKED_INTS[name]
+    no, words, n = ra._PACKED[name]
+    fn = ra.lib().ring_attn_paged_packed
+    for arg in ints.split():
+        for off in (1 << 32, -1 << 32, 1 << 62, 1 << 31):
+            args = {**base, arg: (base[arg] or 0) + off}
+            assert fn(no, words.pack(*[0 if v is None else v for v in args.values()]), n, None) == E, (arg, off)
+
+
+def test_binding_refuses_what_is_no_64_bit_integer():
+    with pytest.raises(ValueError, match="64-bit"):
+        ra._launch("ring_attn_page_trim", 0, *[1 << 64] * 10)
