@@ -672,7 +672,8 @@ def ring_attn_decode_paged(q, k_pool, v_pool, block_table, seq_lens, sel=None, n
 def ring_attn_page_bounds(k_pool, block_table, seq_lens, bounds=None, start_lens=None):
     """Minimum and maximum of the keys of every page, per kv head: bounds
     [num_pages,Hkv,2,D], brought up to date for the pages that hold tokens from
-    start_lens[b] on (all pages without it).  Returns bounds."""
+    start_lens[b] on (all pages without it; none of a sequence whose entry is
+    negative).  Returns bounds."""
     dev = _one_device(k_pool, block_table, seq_lens, bounds, start_lens)
     N, ps, Hkv, D, sp, st, sh = _pool(k_pool)
     B = seq_lens.numel()

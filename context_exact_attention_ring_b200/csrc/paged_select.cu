@@ -66,7 +66,9 @@ __global__ void __launch_bounds__(pgb::THREADS) page_bounds_kernel(BoundsArgs a)
   constexpr int U = 8;                   // rows in flight (pages hold at least 8)
   const int b = blockIdx.y, ps = 1 << a.ps_log2;
   const int len = min(max(a.seq_lens[b], 0), a.W << a.ps_log2);
-  const int p0 = (a.start_lens ? max(a.start_lens[b], 0) : 0) >> a.ps_log2;
+  const int start = a.start_lens ? a.start_lens[b] : 0;
+  if (start < 0) return;      // no new tokens
+  const int p0 = start >> a.ps_log2;
   const int np = (len + ps - 1) >> a.ps_log2;
   const int nc = a.Hkv * a.D / E, step = gridDim.x * pgb::THREADS;
   const int dp = step / nc, dc = step - dp * nc;

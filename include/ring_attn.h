@@ -559,8 +559,9 @@ ring_status ring_attn_decode_paged(const void* q, const void* k_pool, const void
  * bounds [num_pages, Hkv, 2, D] of dtype: [.., 0, :] the minimum, [.., 1, :]
  * the maximum (a NaN among the keys makes both NaN).  Written for the pages of
  * each sequence that hold tokens from start_lens[b] on (from 0 if start_lens
- * is NULL, as after a prompt; < 0 counts as 0), over all valid keys of the
- * page; the other pages' bounds are not touched.  A page that two sequences
+ * is NULL, as after a prompt; none if it is negative, as ring_attn_page_extend
+ * leaves it for a sequence without room), over all valid keys of the page; the
+ * other pages' bounds are not touched.  A page that two sequences
  * share must be full in both.
  * Errors as ring_attn_paged_append, plus RING_EUNSUPPORTED for B > 65535.
  * The source pages have no counterpart.

@@ -103,3 +103,27 @@ def test_slot_map_of_2_to_the_31_entries():
     for at in range(210, T, 1 << 28):
         part = slots[at:at + (1 << 28)]
         assert int(part.min()) == int(part.max()) == -1, at
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_bounds_of_sequences_without_new_tokens_are_left(dtype):
+    # start_lens as page_extend leaves it: -1 for a sequence that found no room; its keys are not looked at
+    need_cuda()
+    ps, Hkv, D, lens = 16, 2, 64, [40, 48, 5, 33]
+    k = torch.randn((16, ps, Hkv, D), device="cuda").to(dtype)
+    tb = ints([[0, 1, 2, 15], [3, 4, 5, 15], [6, 15, 15, 15], [7, 8, 9, 15]])
+    sl, nf = ints(lens), ints([1])
+    slots, start, cu = ra.ring_attn_page_extend(sl, ints([1, 1, 5, 40]), tb, ints([10]), nf, ps, max_tokens=47)
+    torch.cuda.synchronize()
+    assert ra.ring_attn_device_error()[0] == ra.RING_ECAPACITY and start.tolist() == [40, 48, 5, -1]
+    bnd = torch.full((16, Hkv, 2, D), 77.0, device="cuda", dtype=dtype)
+    ra.ring_attn_page_bounds(k, tb, sl, bounds=bnd, start_lens=start)
+    torch.cuda.synchronize()
+    want = torch.full_like(bnd, 77.0).cpu()
+    for pg, x in R.bounds(k, tb[:3], sl[:3].tolist(), start[:3].tolist()).items():
+        want[pg] = x
+    assert torch.equal(bnd.cpu(), want)
+    # any negative start is "nothing new"
+    ra.ring_attn_page_bounds(k, tb, sl, bounds=bnd.fill_(77.0), start_lens=ints([-1, -2 ** 31, -1, -7]))
+    torch.cuda.synchronize()
+    assert (bnd == 77.0).all() and ra.ring_attn_device_error()[0] == ra.RING_OK
