@@ -15,7 +15,7 @@
 
 namespace ra {
 
-__device__ unsigned int g_error_word = 0;
+__device__ unsigned int g_error_word[2] = {0, 0};   // expired waits; lack of room
 
 unsigned int* error_word() {
   int dev = 0;
@@ -28,6 +28,11 @@ unsigned int* error_word() {
     if (cudaGetSymbolAddress(&p, g_error_word) == cudaSuccess) cache[dev] = static_cast<unsigned int*>(p);
   }
   return cache[dev];
+}
+
+unsigned int* capacity_word() {
+  unsigned int* w = error_word();
+  return w ? w + 1 : nullptr;
 }
 
 EncodeTiledFn get_encode_tiled() {
@@ -438,7 +443,7 @@ ring_status ring_attn_kv_append(void* k_cache, void* v_cache, const void* k_new,
   a.k_cache = k_cache; a.v_cache = v_cache; a.k_new = k_new; a.v_new = v_new;
   a.shard_lens = shard_lens; a.n_appended = n_appended;
   a.B = B; a.T = T; a.Hkv = Hkv; a.Smax = Smax; a.D = D; a.P = P; a.block = block; a.elem_bytes = eb;
-  a.err = error_word();
+  a.err = capacity_word();
   return from_cuda(launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -507,12 +512,13 @@ ring_status ring_attn_device_error(int* where) {
   if (where) *where = 0;
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return RING_ECUDA;
-  unsigned int word = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&word, g_error_word, sizeof(word)) != cudaSuccess) return RING_ECUDA;
-  if (word) {
-    if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero)) != cudaSuccess) return RING_ECUDA;
-    if (where) *where = (int)word;
-    return word == kFaultCapacity ? RING_ECAPACITY : RING_ETIMEOUT;
+  unsigned int word[2] = {0, 0}, zero = 0;
+  if (cudaMemcpyFromSymbol(word, g_error_word, sizeof(word)) != cudaSuccess) return RING_ECUDA;
+  for (int i = 0; i < 2; ++i) {
+    if (!word[i]) continue;
+    if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero), i * sizeof(zero)) != cudaSuccess) return RING_ECUDA;
+    if (where) *where = (int)word[i];
+    return i ? RING_ECAPACITY : RING_ETIMEOUT;
   }
   return RING_OK;
 }

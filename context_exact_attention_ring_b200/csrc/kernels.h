@@ -103,7 +103,7 @@ struct AppendArgs {
   int32_t* shard_lens;  // [B,P], read and advanced
   int32_t* n_appended;  // [B], read and advanced
   int B, T, Hkv, Smax, D, P, block, elem_bytes;
-  unsigned int* err;    // device error word (capacity overflow)
+  unsigned int* err;    // capacity word
 };
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st);
 
@@ -127,7 +127,10 @@ bool make_tmap_striped(CUtensorMap* m, const void* base, int B, int S, int P, in
 
 int num_sms();
 
-// Device address of the library's error word on the current device.
+// Device addresses on the current device: of the library's error word, and of
+// the word for lack of room (a full shard, no free page), which is ordinary
+// and may not hide an expired wait.
 unsigned int* error_word();
+unsigned int* capacity_word();
 
 }  // namespace ra

@@ -9,7 +9,7 @@
 // shard_lens[b][p] valid rows; a token is written at the shard's fill count,
 // which then advances.  One CTA per sequence; each warp copies whole token
 // rows with 16-byte loads and stores.  A token whose shard is full is not
-// written: the kernel records kFaultCapacity in the device error word, never
+// written: the kernel records kFaultCapacity in the capacity word, never
 // writes outside the shard, and leaves that shard's count at C.
 #include <cuda_runtime.h>
 
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
     const int len0 = min(max(a.shard_lens[b * a.P + p], 0), C);
     const long long row = len0 + rr_count(n, p, a.block, a.P) - rr_count(n0, p, a.block, a.P);
     if (row >= C) {
-      if (lane == 0) atomicCAS(a.err, 0u, kFaultCapacity);
+      if (lane == 0 && a.err) atomicCAS(a.err, 0u, kFaultCapacity);
       continue;
     }
     const size_t src = ((size_t)b * a.T + j) * row_bytes;

@@ -63,7 +63,7 @@ struct ExtendArgs {
   int32_t* cu_new;            // [B + 1]
   long long table_stride;
   int B, W, ps_log2, max_free, max_tokens;
-  unsigned int* err;
+  unsigned int* err;          // capacity word
 };
 cudaError_t launch_page_extend(const ExtendArgs& a, cudaStream_t st);
 
@@ -75,7 +75,7 @@ struct TrimArgs {
   int32_t* n_free;
   long long table_stride;
   int B, W, ps_log2, max_free;
-  unsigned int* err;
+  unsigned int* err;          // capacity word
 };
 cudaError_t launch_page_trim(const TrimArgs& a, cudaStream_t st);
 

@@ -80,7 +80,7 @@ ring_status ring_attn_page_extend(int32_t* seq_lens, const int32_t* new_lens, in
   a.slot_map = slot_map; a.start_lens = start_lens; a.cu_new = cu_new;
   a.table_stride = (long long)table_stride;
   a.B = B; a.W = W; a.ps_log2 = pl; a.max_free = max_free; a.max_tokens = max_tokens;
-  a.err = error_word();
+  a.err = capacity_word();
   return from_cuda(launch_page_extend(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -98,7 +98,7 @@ ring_status ring_attn_page_trim(int32_t* seq_lens, const int32_t* keep_lens, con
   a.seq_lens = seq_lens; a.keep_lens = keep_lens; a.table = block_table; a.free_pages = free_pages; a.n_free = n_free;
   a.table_stride = (long long)table_stride;
   a.B = B; a.W = W; a.ps_log2 = pl; a.max_free = max_free;
-  a.err = error_word();
+  a.err = capacity_word();
   return from_cuda(launch_page_trim(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

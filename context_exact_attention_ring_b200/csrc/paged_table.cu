@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(pgt::THREADS, 1) page_extend_kernel(ExtendArgs
     for (int w = 1; w < NW; ++w) taken = max(taken, s.warp[w]);
     *a.n_free = n_free - (int)taken;
   }
-  if (full || !is_page((int)largest, a.ps_log2)) atomicCAS(a.err, 0u, kFaultCapacity);
+  if ((full || !is_page((int)largest, a.ps_log2)) && a.err) atomicCAS(a.err, 0u, kFaultCapacity);
 }
 
 // Slots [first, first + SLOT_THREADS * SLOTS) by each block: a warp finds the
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(pgt::THREADS, 1) page_trim_kernel(TrimArgs a) 
   }
   if (tid == 0) {
     *a.n_free = (int)min(base, (long long)a.max_free);
-    if (base > a.max_free) atomicCAS(a.err, 0u, kFaultCapacity);
+    if (base > a.max_free && a.err) atomicCAS(a.err, 0u, kFaultCapacity);
   }
 }
 

@@ -643,11 +643,12 @@ ring_status ring_attn_sched_stats(int S, int P, int causal, int layout, int tile
 
 /*
  * ring_attn_device_error -- synchronise the current device and read-and-clear
- * the library's device error word.  Returns RING_ETIMEOUT if a bounded wait
+ * the library's device error words.  Returns RING_ETIMEOUT if a bounded wait
  * in any kernel expired since the last call, RING_ECAPACITY if a KV append
  * dropped a token because its shard was full or ring_attn_page_extend /
- * _page_trim ran out of room, RING_ECUDA if the device
- * reports an error, else RING_OK.  `where` (may be NULL) receives the code
+ * _page_trim ran out of room, RING_ECUDA if the device reports an error, else
+ * RING_OK.  Of an expired wait and a lack of room the wait is reported (and
+ * cleared) first, the lack of room by the next call.  `where` (may be NULL) receives the code
  * of the site that recorded the error (0 if none).  Code 12 (reported as
  * RING_ETIMEOUT: the kernel unwound without results) means a CTA pair of the
  * prefill kernel found its cluster ranks numbered otherwise than the blocks

@@ -127,3 +127,27 @@ def test_bounds_of_sequences_without_new_tokens_are_left(dtype):
     ra.ring_attn_page_bounds(k, tb, sl, bounds=bnd.fill_(77.0), start_lens=ints([-1, -2 ** 31, -1, -7]))
     torch.cuda.synchronize()
     assert (bnd == 77.0).all() and ra.ring_attn_device_error()[0] == ra.RING_OK
+
+
+@pytest.mark.parametrize("full", ["extend", "trim", "kv_append"])
+def test_an_expired_wait_is_reported_beside_a_full_list(full):
+    # a lack of room is everyday business; it hides no wait that ran out, before it or after it
+    need_cuda()
+    assert ra.ring_attn_device_error()[0] == ra.RING_OK
+
+    def lack():
+        if full == "extend":
+            ra.ring_attn_page_extend(ints([0]), ints([5]), ints([[0]]), ints([0]), ints([0]), 16, max_tokens=5)
+        elif full == "trim":
+            ra.ring_attn_page_trim(ints([5]), ints([0]), ints([[0]]), ints([0]), ints([1]), 16)
+        else:
+            c, new = torch.zeros((1, 4, 1, 8), device="cuda"), torch.zeros((1, 2, 1, 8), device="cuda")
+            ra.ring_attn_kv_append(c, c.clone(), new, new, ints([[4]]), ints([4]), 1, 4)
+
+    for first, second in ((lack, lambda: ra.ring_attn_selftest_wait(1000)), (lambda: ra.ring_attn_selftest_wait(1000), lack)):
+        first()
+        second()
+        st, where = ra.ring_attn_device_error()
+        assert st == ra.RING_ETIMEOUT and where == 11
+        assert ra.ring_attn_device_error()[0] == ra.RING_ECAPACITY
+        assert ra.ring_attn_device_error() == (ra.RING_OK, 0)
