@@ -425,7 +425,9 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
         if (h >= fhd.nh) continue;
         const float4 r = *reinterpret_cast<const float4*>(sm.suml[ob][h]);
         const float L = (r.x + r.y) + (r.z + r.w);
-        const float od = L == 0.f ? 0.f : __fdividef(o[h] + olo[h], L);
+        // an infinite value times a second term, 0 or of either sign, is no part of the result
+        const float oh = fabsf(o[h]) < CUDART_INF_F ? o[h] + olo[h] : o[h];
+        const float od = L == 0.f ? 0.f : __fdividef(oh, L);
         if (row >= DH) continue;      // D = 64: the upper half of O^T is padding
         if (whole)
           paged_store(a, (bh0 + h) * DH + row, od);

@@ -151,3 +151,37 @@ def test_an_expired_wait_is_reported_beside_a_full_list(full):
         assert st == ra.RING_ETIMEOUT and where == 11
         assert ra.ring_attn_device_error()[0] == ra.RING_ECAPACITY
         assert ra.ring_attn_device_error() == (ra.RING_OK, 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 4, 1), (128, 16, 2), (128, 12, 1), (64, 2, 2)])
+@pytest.mark.parametrize("lens", [[300, 200], [9000, 40, 700]])
+def test_decode_infinite_values(dtype, D, Hq, Hkv, lens):
+    # a valid key's infinite value makes its dims infinite in every head, both signs make them NaN; the rest is as without
+    need_cuda()
+    ps = 16
+    W = R.cdiv(max(lens), ps)
+    g = torch.Generator().manual_seed(D + Hq)
+    N = sum(R.cdiv(n, ps) for n in lens)
+    k, v = (torch.randn((N, ps, Hkv, D), generator=g).to(dtype).cuda() for _ in range(2))
+    tb, at = torch.full((len(lens), W), -1, dtype=torch.int32), 0
+    for b, n in enumerate(lens):
+        tb[b, :R.cdiv(n, ps)] = torch.arange(at, at + R.cdiv(n, ps))
+        at += R.cdiv(n, ps)
+    q = torch.randn((len(lens), Hq, D), generator=g).to(dtype).cuda()
+    pos, neg, both = 5, 9, D - 1
+    last = R.cdiv(lens[0], ps) - 2
+    bad = v.clone()
+    bad[2, 3, :, pos], bad[2, 4, :, neg], bad[2, 5, :, both], bad[last, 0, :, both] = (
+        float("inf"), -float("inf"), float("inf"), -float("inf"))
+    for out_dtype in {dtype, torch.float32}:
+        ws = ra.decode_paged_workspace(D)
+        want, lse0 = ra.ring_attn_decode_paged(q, k, v, tb.cuda(), ints(lens), workspace=ws, out_dtype=out_dtype)
+        out, lse = ra.ring_attn_decode_paged(q, k, bad, tb.cuda(), ints(lens), workspace=ws, out_dtype=out_dtype)
+        torch.cuda.synchronize()
+        assert ra.ring_attn_device_error()[0] == ra.RING_OK
+        assert torch.isposinf(out[0, :, pos]).all() and torch.isneginf(out[0, :, neg]).all()
+        assert torch.isnan(out[0, :, both]).all() and torch.equal(lse, lse0)
+        rest = torch.ones(out.shape, dtype=torch.bool, device="cuda")
+        rest[0, :, [pos, neg, both]] = False
+        assert torch.equal(out[rest], want[rest])
