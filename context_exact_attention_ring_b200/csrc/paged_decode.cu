@@ -51,7 +51,7 @@ constexpr int SLAB = kPagedTile * 128;      // 128 rows x 64 columns of bf16 (16
 constexpr int QSLAB = NQ * 128;
 constexpr int CT = 128;                     // softmax threads
 constexpr int THREADS = CT + 96;
-constexpr uint32_t TMEM_COLS = 128;         // S^T 2 x 16, O^T 2 x (16 or 32)
+constexpr uint32_t TMEM_COLS = 128;         // S^T 2 x 16, O^T 2 x (16 or 32), folded sums of up to 16 heads
 constexpr float LAZY = 8.f;                 // log2 of the growth tolerated before the base moves
 // K/V stages: what shared memory holds (D = 64, 56 sequences of 16,000 keys: 404 us with 3, 395 with 5).
 template <int DH>
@@ -63,6 +63,11 @@ constexpr int MAX_SLOTS = kPagedTile / 8;   // page slots of a tile
 template <int G>
 constexpr int SEG_COST = paged_seg_cost(G);
 constexpr int PARTS_PER_TILE = 20;          // parts joined in the time of a tile
+// Tiles added up in the products' accumulator before it is folded into a float32 sum that rounds: the tensor
+// cores drop what does not fit, always towards zero (float32 outputs of 1M keys to a CTA are off by 9e-4 of
+// themselves without folding, by 1e-5 with 64 tiles, 5e-6 with 32, 3e-6 with 16 and with few keys; 341 us for 6
+// sequences of 64k to 128k keys with any of them).
+constexpr int FOLD = 16;
 }  // namespace pdt
 
 template <int G, int DH>
@@ -136,6 +141,10 @@ __device__ __forceinline__ void paged_tmem_st(uint32_t t, const float (&v)[N]) {
   else
     tmem_st16(t, r);
 }
+
+// The sum of a product's two terms.  An infinite value times a weight's second
+// term, 0 or of either sign, is no part of it.
+__device__ __forceinline__ float paged_terms(float hi, float lo) { return fabsf(hi) < CUDART_INF_F ? hi + lo : hi; }
 
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -396,6 +405,9 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
     PagedHead fhd{};
     float fl[G];
     uint32_t fu = 0;
+    // sums folded so far of the present piece and of the one to be finished: whether there are any
+    bool folded = false, ffolded = false;
+    const uint32_t tA = tmem + lane_off + 32 + 2 * NP;
     auto finish = [&]() -> bool {
       const uint32_t ob = fu & 1u;
       const bool fin = mbar_wait(smem_u32(&sm.o_full[ob]), (fu >> 1) & 1u, abort_flag, kWaitOFinal, err);
@@ -406,6 +418,14 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
       paged_tmem_ld<G>(tO, o);
       paged_tmem_ld<G>(tO + GP, olo);
       tmem_wait_ld();
+#pragma unroll
+      for (int h = 0; h < G; ++h) o[h] = paged_terms(o[h], olo[h]);
+      if (ffolded) {
+        paged_tmem_ld<G>(tA, olo);
+        tmem_wait_ld();
+#pragma unroll
+        for (int h = 0; h < G; ++h) o[h] += olo[h];
+      }
       tc_fence_before();
       mbar_arrive(smem_u32(&sm.o_free[ob]));
       ++fu;
@@ -425,9 +445,7 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
         if (h >= fhd.nh) continue;
         const float4 r = *reinterpret_cast<const float4*>(sm.suml[ob][h]);
         const float L = (r.x + r.y) + (r.z + r.w);
-        // an infinite value times a second term, 0 or of either sign, is no part of the result
-        const float oh = fabsf(o[h]) < CUDART_INF_F ? o[h] + olo[h] : o[h];
-        const float od = L == 0.f ? 0.f : __fdividef(oh, L);
+        const float od = L == 0.f ? 0.f : __fdividef(o[h], L);
         if (row >= DH) continue;      // D = 64: the upper half of O^T is padding
         if (whole)
           paged_store(a, (bh0 + h) * DH + row, od);
@@ -540,11 +558,52 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
               for (int h = 0; h < G; ++h) o[h] *= alpha[h];
               paged_tmem_st<G>(tO + part * GP, o);
             }
+            if (folded) {
+              paged_tmem_ld<G>(tA, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int h = 0; h < G; ++h) o[h] *= alpha[h];
+              paged_tmem_st<G>(tA, o);
+            }
             tmem_wait_st();
             if (named_bar_any(1, CT, !good)) {
               ok = false;
               break;
             }
+          }
+        }
+        if (j > pc.a && (j - pc.a) % FOLD == 0) {      // the same in every thread
+          const uint32_t tp = t - 1;
+          good = mbar_wait(smem_u32(&sm.o_done[tp & 1u]), (tp >> 1) & 1u, abort_flag, kWaitPFull, err);
+          __syncwarp();
+          tc_fence_after();
+          const uint32_t tO = tmem + lane_off + 32 + (nu & 1u) * NP;
+          constexpr int C = G < 4 ? G : 4;
+#pragma unroll
+          for (int h0 = 0; h0 < G; h0 += C) {
+            float x[C], y[C];
+            paged_tmem_ld<C>(tO + h0, x);
+            paged_tmem_ld<C>(tO + GP + h0, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < C; ++h) x[h] = paged_terms(x[h], y[h]);
+            if (folded) {
+              paged_tmem_ld<C>(tA + h0, y);
+              tmem_wait_ld();
+#pragma unroll
+              for (int h = 0; h < C; ++h) x[h] += y[h];
+            }
+            paged_tmem_st<C>(tA + h0, x);
+#pragma unroll
+            for (int h = 0; h < C; ++h) x[h] = 0.f;
+            paged_tmem_st<C>(tO + h0, x);
+            paged_tmem_st<C>(tO + GP + h0, x);
+          }
+          tmem_wait_st();
+          folded = true;
+          if (named_bar_any(1, CT, !good)) {
+            ok = false;
+            break;
           }
         }
         // weights against the base, as two bf16 terms, for the tensor cores
@@ -574,6 +633,8 @@ __global__ void __launch_bounds__(pdt::THREADS, 1)
       if (!ok) break;
       fpc = pc;
       fhd = paged_head(a, pc.row, pc.sub, NQ);
+      ffolded = folded;
+      folded = false;
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         if (row == 0) sm.base[nu & 1u][h] = m[h];

@@ -8,7 +8,7 @@ import torch
 
 import context_exact_attention_ring_b200 as ra
 from tests import paged_ref as R
-from tests.helpers import need_cuda
+from tests.helpers import margin, need_cuda
 
 pytestmark = pytest.mark.gpu
 
@@ -185,3 +185,37 @@ def test_decode_infinite_values(dtype, D, Hq, Hkv, lens):
         rest = torch.ones(out.shape, dtype=torch.bool, device="cuda")
         rest[0, :, [pos, neg, both]] = False
         assert torch.equal(out[rest], want[rest])
+
+
+@pytest.mark.parametrize("n,Hq,D,ramp", [(1000003, 2, 128, 0.0), (400001, 16, 64, 0.0), (300007, 4, 128, 24.0),
+                                         (100000, 9, 64, 24.0), (130001, 1, 128, 24.0), (70000, 8, 64, 0.0)])
+def test_decode_sums_of_many_keys_to_a_cta(n, Hq, D, ramp):
+    # more sequences than CTAs, all on the same pages, so that a CTA adds up whole sequences; values of one sign, so
+    # that sums which lose their last bits are off by as much as they lose.  With a ramp the scores grow along the
+    # sequence, and the running maximum with them.
+    need_cuda()
+    ps, B = 64, 150
+    N = R.cdiv(n, ps)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k = torch.randn((N, ps, 1, D), generator=g, device="cuda").to(torch.bfloat16)
+    if ramp:
+        k[..., 0] = torch.linspace(0, ramp, N * ps, device="cuda").view(N, ps, 1).to(torch.bfloat16)
+    v = (0.5 + torch.rand((N, ps, 1, D), generator=g, device="cuda")).to(torch.bfloat16)
+    q = torch.randn((B, Hq, D), generator=g, device="cuda").to(torch.bfloat16)
+    q[..., 0] = 16.0 if ramp else q[..., 0]
+    tb = torch.randperm(N, generator=g, device="cuda").to(torch.int32)
+    out, lse = ra.ring_attn_decode_paged(q, k, v, tb.repeat(B, 1), ints([n] * B), out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert ra.ring_attn_device_error()[0] == ra.RING_OK
+    scale = 1 / math.sqrt(D)
+    kk, vv = (x[tb.long()].view(-1, D)[:n].double() for x in (k, v))
+    for b in (0, 77, B - 1):
+        x = q[b].double() @ kk.T * scale
+        s = D * 2.0 ** -23 * float((q[b].double().abs() @ kk.abs().T).max() * scale)
+        want, l = torch.softmax(x, -1) @ vv, torch.logsumexp(x, -1)
+        # the scores' error s, in a weight and in the sum of all; the weights' second terms, 2^-16, and exponentials,
+        # 2^-20; up to 16 tiles of 128 terms that drop a last bit each, 2^-23, and then sums that round: one per 16
+        # tiles in the outputs, one per tile in the weights'
+        tol = 2 * s + 2.0 ** -15 + 16 * 128 * 2.0 ** -23 + (n / 2048 + n / 128 + 20) * 2.0 ** -24
+        margin("out", ((out[b].double() - want) / want).abs().max(), tol)
+        margin("lse", (lse[b].double() - l).abs().max(), s + 2.0 ** -18 + (n / 128 + 20) * 2.0 ** -24 + 2.0 ** -21 * float(l.abs().max()))
