@@ -21,7 +21,7 @@ enum WaitSite : unsigned int {
   kWaitDecodeFull = 9, kWaitDecodeEmpty = 10, kWaitSelftest = 11,
   kPairRank = 12,   // not a wait: a CTA pair found its cluster ranks laid out otherwise than assumed
 };
-// In the capacity word: a KV append dropped a token, or a page call ran out of room.
+// Not a wait: a KV append found the target shard full and dropped the token.
 constexpr unsigned int kFaultCapacity = 0x100;
 
 // Two seconds: far above any legitimate wait inside these kernels.
