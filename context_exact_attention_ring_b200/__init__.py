@@ -623,7 +623,8 @@ def ring_attn_decode_paged_workspace_bytes(D) -> int:
 
 
 def decode_paged_workspace(D, device="cuda"):
-    """A zeroed workspace for ring_attn_decode_paged (one per stream; allocated with torch)."""
+    """A zeroed workspace for ring_attn_decode_paged (one per stream; allocated with
+    torch and zeroed on the current stream)."""
     n = ring_attn_decode_paged_workspace_bytes(D)
     if n == 0:
         raise ValueError("bad head dimension")
@@ -690,8 +691,9 @@ def ring_attn_page_bounds(k_pool, block_table, seq_lens, bounds=None, start_lens
 
 
 def ring_attn_page_scores(q, bounds, block_table, seq_lens, page_size, scores=None):
-    """scores [B,Hkv,W]: for every page an upper bound of q . k over its keys and
-    the query heads of the kv head (-inf past the sequence's pages)."""
+    """scores [B,Hkv,W]: for every page an upper bound (up to float32 rounding) of
+    q . k over its keys and the query heads of the kv head (-inf past the
+    sequence's pages)."""
     dev = _one_device(q, bounds, block_table, seq_lens, scores)
     if q.dim() != 3 or bounds.dim() != 4 or bounds.shape[2] != 2 or not bounds.is_contiguous():
         raise ValueError("q [B, Hq, D] and contiguous bounds [num_pages, Hkv, 2, D] expected")

@@ -52,7 +52,7 @@ ring_status pool_check(const void* pool, int num_pages, int ps_log2, int Hkv, in
   if (D != 64 && D != 128) return RING_EUNSUPPORTED;
   const int eb = elem_bytes(dtype);
   if (!good_stride(sp, eb) || !good_stride(st, eb) || !good_stride(sh, eb)) return RING_EINVAL;
-  // rows of different heads, tokens and pages may not overlap
+  // rows next to each other in any dimension do not overlap (strides of two dimensions together are not compared)
   if (st < (size_t)D || (Hkv > 1 && sh < (size_t)D) || (num_pages > 1 && sp < (size_t)D)) return RING_EINVAL;
   out->page = (long long)sp;
   out->token = (long long)st;

@@ -8,12 +8,13 @@
 //   O^T += V^T P^T    M = 128 dims, N = 2 x 8 or 2 x 16, K = 128 keys
 // N = 16 is the narrowest product, so 8 heads leave half of its columns
 // empty: the weights go in as two bf16 terms, p = hi + lo with |p - hi - lo|
-// <= 2^-16 p, in columns of their own, and the output is float32-accurate up
-// to its own rounding for the price of the second shared-memory store.
+// <= 2^-16 p, in columns of their own, for the price of the second
+// shared-memory store.  Every FOLD tiles O^T is added to a sum beside it in
+// tensor memory.  The float32 output is off by 2e-6 to 4e-6 of itself.
 //
 // Bound by HBM: a tile is 64 KB at D = 128 against 2 x 128 x 16 x D products
-// (6 sequences of 64k to 128k keys, 32/8 heads of 128: 348 us, 6.7 TB/s; 64 ragged
-// ones of 64 to 16,000: 104 us, 6.0 TB/s; one of 77 keys: 6.3 us).
+// (6 sequences of 64k to 128k keys, 32/8 heads of 128: 346 us, 6.7 TB/s; 64 ragged
+// ones of 64 to 16,000: 103 us, 6.0 TB/s; one of 77 keys: 5.9 us).
 // One CTA per SM; warp roles:
 //   warps 0-3  softmax: thread t owns tensor-memory lane t (key row t of S^T,
 //              dim t of O^T);
@@ -64,9 +65,9 @@ template <int G>
 constexpr int SEG_COST = paged_seg_cost(G);
 constexpr int PARTS_PER_TILE = 20;          // parts joined in the time of a tile
 // Tiles added up in the products' accumulator before it is folded into a float32 sum that rounds: the tensor
-// cores drop what does not fit, always towards zero (float32 outputs of 1M keys to a CTA are off by 9e-4 of
-// themselves without folding, by 1e-5 with 64 tiles, 5e-6 with 32, 3e-6 with 16 and with few keys; 341 us for 6
-// sequences of 64k to 128k keys with any of them).
+// cores drop what does not fit, always towards zero.  1M keys to a CTA: outputs off by 9e-4 of themselves (6.5e-3
+// with values of one sign) without folding, 1e-5 with 64 tiles, 5e-6 with 32, 3e-6 with 16 (4e-6 with values of
+// one sign), about as with few keys; the times are the same (6 sequences of 64k to 128k keys).
 constexpr int FOLD = 16;
 }  // namespace pdt
 

@@ -12,9 +12,10 @@
 // one's V is used, its V during the next scores.  The 8 partial scores of a head
 // are added up across the lanes by halving (4 + 2 + 1 exchanges leave a lane one
 // key), so that a lane takes one maximum and one exponential per head; the
-// weights return through shared memory as pairs.  Bound by the instructions of a head
-// and 8 keys, and their latencies, above two heads (issue slots 44% busy with
-// 5), and by memory below.
+// weights return through shared memory as pairs.  Above two heads bound by the
+// latency of a head's chain (exchanges, maximum, a branch, exponential) and of
+// a piece's start, when the copies' pipeline is empty (with 5 heads issue slots
+// are 44% busy, DRAM 50%), and by memory below.
 // (Four keys at a time: 62 us for 400,000 rows of 5 heads of 64, eight: 57, with
 // the runs weighed as now 48.)
 #include <cuda_runtime.h>

@@ -4,7 +4,7 @@
 //          the page's valid keys (comparisons only: exact in the cache's type).
 // scores   score(page) = max over the heads h of the group of
 //            sum_d max(q_hd lo_d, q_hd hi_d) >= max_h max_{key in page} q_h . k,
-//          so no key of a page scores above it.
+//          so no key of a page scores above it but by the rounding of float32 sums.
 // select   the K best pages of a (sequence, kv head), in ascending order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -127,8 +127,9 @@ cudaError_t launch_page_bounds(const BoundsArgs& a, cudaStream_t st) {
 // queries wait in shared memory, so that any number of heads takes one pass.
 // max(q lo, q hi) is q times hi or lo by the sign of q: a select and an FMA.
 // The two pages' sums are added up across the half-warp by halving: after one
-// exchange a lane has one page.  (142,000 pages' bounds of 128 dims, 73 MB, and
-// 4 heads: 29 us, issue slots 54% busy; four pages at half the occupancy: 40 us.)
+// exchange a lane has one page.  (131,000 pages' bounds of 128 dims, 67 MB, and
+// 4 heads: 28 us, issue slots 55% busy; four pages at half the occupancy took 12 us
+// more.  From L2 21 us, with 8 heads 32, with 16 heads 55: instructions bound it.)
 // ---------------------------------------------------------------------------
 namespace pgsc {
 constexpr int THREADS = 256;
@@ -253,11 +254,11 @@ cudaError_t launch_page_scores(const ScoresArgs& a, bool bf16, cudaStream_t st) 
 // ---------------------------------------------------------------------------
 // selection.  A block per (sequence, kv head).  Scores become 32-bit keys of
 // the same order, kept in shared memory 8192 at a time; three passes of 11,
-// 11 and 10 bits narrow down the K-th largest key (a histogram of 2048 bins
-// keeps the atomics apart, and the block sums it from the top), and one ordered pass writes the
-// pages above it and the first ones equal to it.  Latency-bound: a list is a
-// few KB (48 lists of up to 4096: 8 us; with four passes of 8 bits over 256 bins
-// that one thread summed, 26 us).
+// 11 and 10 bits narrow down the K-th largest key (the block sums a histogram of
+// 2048 bins from the top), and one ordered pass writes the pages above it and the
+// first ones equal to it.  Latency-bound: a list is a few KB (48 lists of up to 4096:
+// 8 us, whether the keys fall into 85 bins of the first pass, into two, or are all
+// alike; with four passes of 8 bits over 256 bins that one thread summed, 26 us).
 // ---------------------------------------------------------------------------
 namespace pgse {
 constexpr int THREADS = 1024;

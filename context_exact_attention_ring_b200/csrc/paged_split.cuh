@@ -72,7 +72,8 @@ struct PagedRunSmem {
 // The number of CTAs for run.T units in segs segments, and this CTA's run.
 // parts_per_tile: how many parts a segment may be cut into for every tile of
 // a part.  Joining takes as long as a tile for every parts_per_tile parts, so
-// that cutting n parts of T / n tiles is longest at n^2 = parts_per_tile T.
+// that the time with n parts, T / n + n / parts_per_tile, is shortest at
+// n^2 = parts_per_tile T.
 __device__ __forceinline__ void paged_cut(PagedRun& run, int segs, int seg_cost, int parts_per_tile) {
   const int tiles = run.T - segs * seg_cost, c = blockIdx.x;
   run.n = max(1, min(min((int)gridDim.x, tiles), (int)sqrtf((float)parts_per_tile * tiles * segs)));

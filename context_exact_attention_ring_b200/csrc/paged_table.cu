@@ -91,7 +91,7 @@ struct ScanSmem {
 // by bisection.  More, a warp takes a sequence's first 128, four sequences'
 // 64 in flight at once, and the block together the rest of the long ones.
 // (Extend and trim of 256 sequences with 40 pages: 7.5 us by bisection, 10 the
-// other way; of 1021 sequences with 33,000 pages: 65 and 36 us.)  Called by all
+// other way; of 1021 sequences with 33,000 pages: 65 and 33 us.)  Called by all
 // threads between barriers.
 template <typename Load, typename Store>
 __device__ __forceinline__ void move_pages(ScanSmem& s, int n, long long total, Load load, Store store) {

@@ -577,8 +577,8 @@ ring_status ring_attn_page_bounds(const void* k_pool, void* bounds, const int32_
  * scores [B,Hkv,W] float: for page i of sequence b and kv head g, with
  * (lo, hi) the bounds of its pool page, the largest over the query heads h of
  * the group of sum_d max(q[b,h,d] lo_d, q[b,h,d] hi_d): no key of the page has
- * a larger q . k.  -inf from the sequence's last page on and for table entries
- * outside the pool.  q as in ring_attn_decode_paged.
+ * a larger q . k, up to the rounding of a float32 sum of D products.  -inf past
+ * the sequence's last page and for table entries outside the pool.  q as in ring_attn_decode_paged.
  * Errors as ring_attn_page_bounds, plus RING_EUNSUPPORTED for Hq / Hkv > 64
  * or B * Hkv > 65535.
  * The source pages have no counterpart.
