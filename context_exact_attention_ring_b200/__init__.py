@@ -773,7 +773,8 @@ def ring_attn_selftest_wait(limit_us=1000):
 
 
 def ring_attn_device_error():
-    """Synchronise and return (status, site) of the device error word (cleared)."""
+    """Synchronise and return (status, site) of the device error words; what is
+    reported is cleared (an expired wait first, lack of room by the next call)."""
     where = ctypes.c_int(0)
     st = lib().ring_attn_device_error(ctypes.byref(where))
     return st, where.value
